@@ -23,6 +23,18 @@ anything else.
     o = recurrent_decode_multi(q, k, v, g, beta, cu_seqlens, state_pool, state_indices,
                                intermediate_states=cache, update_pool=False)
 
+    # the steps beside them: short causal convolution, selective state-space scan, draft verification
+    y, conv_pool = conv_prefill(x, weight, bias, cu_seqlens, initial_state=conv_pool, state_indices=idx)
+    y = conv_decode(x, weight, bias, conv_pool, state_indices)
+    y, pool = ssm_prefill(x, dt, A_log, B, C, cu_seqlens, D=D, z=z, dt_bias=dt_bias,
+                          initial_state=pool, state_indices=idx)
+    y = ssm_decode(x, dt, A_log, B, C, state_pool, state_indices, D=D, z=z, dt_bias=dt_bias)
+    y = ssm_decode_multi(x, dt, A_log, B, C, cu_seqlens, state_pool, state_indices, intermediate_states=cache)
+    accepted, next_tokens, emitted = verify_drafts(tokens, target_probs, cu_seqlens, uniform, uniform_next,
+                                                   draft_probs=draft_probs)
+    commit_states(state_pool, state_indices, cache, accepted)     # either decode's step cache
+    conv_commit(x, cu_seqlens, accepted, conv_pool, state_indices)
+
 Layouts (contiguous): q, k [T, Hk, K]; v [T, Hv, V]; g [T, Hv, K] (per-channel
 gate) or [T, Hv] (scalar gate); beta [T, Hv] fp32; states [.., Hv, V, K];
 raw x shaped like g and b like beta, both in the io dtype; A_log, dt_bias
@@ -38,6 +50,8 @@ import torch
 __all__ = ["chunk_prefill", "chunk_prefill_noalloc", "recurrent_decode", "chunk_prefill_fused_gate",
            "recurrent_decode_fused_gate", "recurrent_decode_multi", "recurrent_decode_multi_fused_gate",
            "recurrent_decode_packed", "recurrent_decode_packed_fused_gate",
+           "conv_prefill", "conv_decode", "conv_commit", "ssm_prefill", "ssm_decode", "ssm_decode_multi",
+           "verify_drafts", "commit_states",
            "workspace_size", "release_workspaces", "library_path", "KdaError"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -80,6 +94,38 @@ class DecodeDesc(ctypes.Structure):
                 ("num_slots", ctypes.c_int32)]
 
 
+class ConvDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("channels", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("num_slots", ctypes.c_int32), ("update_pool", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64)]
+
+
+class SsmDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("state_dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+                ("num_slots", ctypes.c_int32), ("cache_steps", ctypes.c_int32),
+                ("cache_pitch", ctypes.c_int32), ("update_pool", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64)]
+
+
+class VerifyDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("prob_dtype", ctypes.c_int32),
+                ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64)]
+
+
+class CommitDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+                ("cache_steps", ctypes.c_int32), ("cache_pitch", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int64)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 
@@ -115,6 +161,26 @@ def lib():
         L.kda_recurrent_decode_multi.argtypes = [ctypes.POINTER(MultiDecodeDesc)] + [_P] * 11
         L.kda_recurrent_decode_multi_fused_gate.restype = ctypes.c_int
         L.kda_recurrent_decode_multi_fused_gate.argtypes = [ctypes.POINTER(MultiDecodeDesc)] + [_P] * 13
+        L.kda_conv_prefill.restype = ctypes.c_int
+        L.kda_conv_prefill.argtypes = [ctypes.POINTER(ConvDesc)] + [_P] * 9
+        L.kda_conv_decode.restype = ctypes.c_int
+        L.kda_conv_decode.argtypes = [ctypes.POINTER(ConvDesc)] + [_P] * 7
+        L.kda_conv_commit.restype = ctypes.c_int
+        L.kda_conv_commit.argtypes = [ctypes.POINTER(ConvDesc)] + [_P] * 6
+        L.kda_ssm_prefill_workspace_size.restype = ctypes.c_size_t
+        L.kda_ssm_prefill_workspace_size.argtypes = [ctypes.POINTER(SsmDesc)]
+        L.kda_ssm_prefill.restype = ctypes.c_int
+        L.kda_ssm_prefill.argtypes = [ctypes.POINTER(SsmDesc)] + [_P] * 14 + [ctypes.c_size_t, _P]
+        L.kda_ssm_decode.restype = ctypes.c_int
+        L.kda_ssm_decode.argtypes = [ctypes.POINTER(SsmDesc)] + [_P] * 12
+        L.kda_ssm_decode_multi.restype = ctypes.c_int
+        L.kda_ssm_decode_multi.argtypes = [ctypes.POINTER(SsmDesc)] + [_P] * 14
+        L.kda_verify_drafts_workspace_size.restype = ctypes.c_size_t
+        L.kda_verify_drafts_workspace_size.argtypes = [ctypes.POINTER(VerifyDesc)]
+        L.kda_verify_drafts.restype = ctypes.c_int
+        L.kda_verify_drafts.argtypes = [ctypes.POINTER(VerifyDesc)] + [_P] * 10 + [ctypes.c_size_t, _P]
+        L.kda_commit_states.restype = ctypes.c_int
+        L.kda_commit_states.argtypes = [ctypes.POINTER(CommitDesc)] + [_P] * 5
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_version.restype = ctypes.c_int32
@@ -484,3 +550,282 @@ def recurrent_decode_packed_fused_gate(qkv, gate_x, A_log, dt_bias, beta_x, stat
     _need(dt_bias, "dt_bias", torch.float32, gate_x.dim() - 1)
     return _decode_packed(qkv, (gate_x, A_log, dt_bias, beta_x), state_pool, state_indices, hk, hv, dk, dv,
                           scale, True)
+
+
+# ---- short causal convolution, state-space scan, drafts ---------------------
+
+
+def _token_rows(t, name, dtype, n, tail):
+    """t must be [>= n, *tail], contiguous within a row; rows may lie apart (a
+    slice of a wider row).  Returns the elements between two rows."""
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    _rows(t, name, n, tail)
+    width = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != width:
+            raise ValueError("%s must be contiguous within a row" % name)
+        width *= size
+    if t.shape[0] <= 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError("%s must have rows that do not overlap" % name)
+    return t.stride(0)
+
+
+def _scratch(nbytes, device):
+    """Workspace of one call, from torch's allocator: held by the graph where
+    the call is captured, so that no two graphs or streams share it."""
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def _cu(cu_seqlens):
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    n = cu_seqlens.numel() - 1
+    if n < 0:
+        raise ValueError("cu_seqlens must hold N + 1 >= 1 offsets")
+    return n
+
+
+def _conv_args(x, weight, bias):
+    if x.dim() != 2:
+        raise ValueError("x must be [T, D]")
+    dt = _io_dtype(x)
+    T, D = x.shape
+    _need(weight, "weight", x.dtype, 2)
+    if weight.shape[0] != D:
+        raise ValueError("weight must have shape [%d, W], got %s" % (D, tuple(weight.shape)))
+    _need(bias, "bias", x.dtype, 1)
+    if bias is not None and bias.shape[0] != D:
+        raise ValueError("bias must have shape [%d], got %s" % (D, tuple(bias.shape)))
+    return dt, T, D, weight.shape[1], _token_rows(x, "x", x.dtype, T, (D,))
+
+
+def conv_prefill(x, weight, bias, cu_seqlens, *, initial_state=None, state_indices=None, activation="silu",
+                 output_final_state=True, update_pool=True):
+    """Causal depthwise convolution of packed sequences, y = silu(bias + taps):
+    x [T, D] (rows may be slices of wider ones), weight [D, W], W = 2..4, bias
+    [D] or None.  Returns (y, final_state).
+
+    A state is the last W - 1 inputs [W - 1, D], oldest first, in x's dtype.
+    Dense mode: initial_state [N, W - 1, D] or None (zeros), final_state a new
+    tensor (None when output_final_state is False).  Pool mode: initial_state
+    is the pool [slots, W - 1, D], updated in place at state_indices (negative
+    -> last slot) unless update_pool is False, and returned.  activation:
+    "silu" or None."""
+    dt, T, D, W, stride = _conv_args(x, weight, bias)
+    if activation not in ("silu", None):
+        raise ValueError("activation must be 'silu' or None")
+    N = _cu(cu_seqlens)
+    _need(initial_state, "initial_state", x.dtype, 3)
+    _need(state_indices, "state_indices", torch.int32, 1)
+    pool = state_indices is not None
+    if pool and initial_state is None:
+        raise ValueError("pool mode needs the pool as initial_state")
+    _rows(initial_state, "state pool" if pool else "initial_state", 1 if pool else N, (W - 1, D))
+    _rows(state_indices, "state_indices", N, ())
+    dev = _on_device(x, (weight, bias, cu_seqlens, initial_state, state_indices))
+    desc = ConvDesc(N, T, D, W, dt, 1 if activation else 0, initial_state.shape[0] if pool else 0, 1 if update_pool else 0, stride)
+    y = torch.empty(T, D, dtype=x.dtype, device=dev)
+    final = initial_state if pool else (torch.empty(N, W - 1, D, dtype=x.dtype, device=dev) if output_final_state else None)
+    with torch.cuda.device(dev):
+        _check(lib().kda_conv_prefill(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(initial_state),
+                                      _ptr(state_indices), None if pool else _ptr(final), _ptr(y), _stream(dev)))
+    return y, final
+
+
+def conv_decode(x, weight, bias, conv_pool, state_indices, *, activation="silu"):
+    """One token of B requests through the convolution, in place on the pool
+    [slots, W - 1, D].  Returns y [B, D]."""
+    dt, B, D, W, stride = _conv_args(x, weight, bias)
+    if activation not in ("silu", None):
+        raise ValueError("activation must be 'silu' or None")
+    _need(conv_pool, "conv_pool", x.dtype, 3)
+    _need(state_indices, "state_indices", torch.int32, 1)
+    _rows(conv_pool, "conv_pool", 1, (W - 1, D))
+    _rows(state_indices, "state_indices", B, ())
+    dev = _on_device(x, (weight, bias, conv_pool, state_indices))
+    desc = ConvDesc(B, B, D, W, dt, 1 if activation else 0, conv_pool.shape[0], 1, stride)
+    y = torch.empty(B, D, dtype=x.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().kda_conv_decode(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_pool), _ptr(state_indices),
+                                     _ptr(y), _stream(dev)))
+    return y
+
+
+def conv_commit(x, cu_seqlens, steps, conv_pool, state_indices):
+    """After conv_prefill(..., update_pool=False) over drafted tokens: request
+    n's pool row becomes the last W - 1 inputs up to its token steps[n] (its
+    accepted step; negative, or not below its length: left as it is)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, D]")
+    T, D = x.shape
+    stride = _token_rows(x, "x", x.dtype, T, (D,))
+    N = _cu(cu_seqlens)
+    _need(conv_pool, "conv_pool", x.dtype, 3)
+    _need(state_indices, "state_indices", torch.int32, 1)
+    _need(steps, "steps", torch.int32, 1)
+    _rows(conv_pool, "conv_pool", 1, (conv_pool.shape[1], D))
+    _rows(state_indices, "state_indices", N, ())
+    _rows(steps, "steps", N, ())
+    dev = _on_device(x, (cu_seqlens, steps, conv_pool, state_indices))
+    desc = ConvDesc(N, T, D, conv_pool.shape[1] + 1, _io_dtype(x), 0, conv_pool.shape[0], 1, stride)
+    with torch.cuda.device(dev):
+        _check(lib().kda_conv_commit(ctypes.byref(desc), _ptr(x), _ptr(cu_seqlens), _ptr(steps), _ptr(conv_pool),
+                                     _ptr(state_indices), _stream(dev)))
+
+
+def _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, num_seqs, state_dtype):
+    """Checked descriptor of a scan call over x's token rows."""
+    if x.dim() != 3:
+        raise ValueError("x must be [T, H, P]")
+    if B.dim() != 3:
+        raise ValueError("B must be [T, G, S]")
+    T, H, P = x.shape
+    G, S = B.shape[1], B.shape[2]
+    if G <= 0 or H % G != 0:
+        raise ValueError("heads (%d) must be a multiple of groups (%d)" % (H, G))
+    if state_dtype not in _DT:
+        raise ValueError("states must be float32 or bfloat16")
+    desc = SsmDesc(num_seqs, T, H, G, P, S, _io_dtype(x), _DT[state_dtype], 0, 0, 0, 0)
+    desc.x_stride = _token_rows(x, "x", x.dtype, T, (H, P))
+    desc.dt_stride = _token_rows(dt, "dt", x.dtype, T, (H,))
+    desc.b_stride = _token_rows(B, "B", x.dtype, T, (G, S))
+    desc.c_stride = _token_rows(C, "C", x.dtype, T, (G, S))
+    desc.z_stride = 0 if z is None else _token_rows(z, "z", x.dtype, T, (H, P))
+    for t, name in ((A_log, "A_log"), (D, "D"), (dt_bias, "dt_bias")):
+        _need(t, name, torch.float32, 1)
+        if t is not None and t.shape[0] != H:
+            raise ValueError("%s must have shape [%d], got %s" % (name, H, tuple(t.shape)))
+    return desc
+
+
+def ssm_prefill(x, dt, A_log, B, C, cu_seqlens, *, D=None, z=None, dt_bias=None, initial_state=None,
+                state_indices=None, output_final_state=True, state_dtype=None):
+    """Selective state-space scan over packed sequences: with
+    dt = softplus(dt + dt_bias), state = exp(-exp(A_log) dt) state + dt x B^T,
+    y = (state C + D x) [* silu(z)].  x, z [T, H, P], dt [T, H], B, C
+    [T, G, S], rows sliced from wider ones or not; A_log, D, dt_bias [H] fp32.
+    Returns (y, final_state); dense and pool mode as for chunk_prefill, a state
+    being [H, P, S]."""
+    N = _cu(cu_seqlens)
+    _need(initial_state, "initial_state", None, 4)
+    _need(state_indices, "state_indices", torch.int32, 1)
+    pool = state_indices is not None
+    if pool and initial_state is None:
+        raise ValueError("pool mode needs the pool as initial_state")
+    sd = initial_state.dtype if initial_state is not None else (state_dtype or torch.float32)
+    desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, N, sd)
+    one = (desc.heads, desc.head_dim, desc.state_dim)
+    _rows(initial_state, "state pool" if pool else "initial_state", 1 if pool else N, one)
+    _rows(state_indices, "state_indices", N, ())
+    dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, initial_state, state_indices))
+    desc.num_slots = initial_state.shape[0] if pool else 0
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    final = initial_state if pool else (torch.empty(N, *one, dtype=sd, device=dev) if output_final_state else None)
+    with torch.cuda.device(dev):
+        nbytes = int(lib().kda_ssm_prefill_workspace_size(ctypes.byref(desc)))
+        ws = _scratch(nbytes, dev) if nbytes else None
+        _check(lib().kda_ssm_prefill(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                     _ptr(dt_bias), _ptr(cu_seqlens), _ptr(initial_state), _ptr(state_indices),
+                                     None if pool else _ptr(final), _ptr(y), _ptr(ws), nbytes, _stream(dev)))
+    return y, final
+
+
+def ssm_decode(x, dt, A_log, B, C, state_pool, state_indices, *, D=None, z=None, dt_bias=None):
+    """One token of every request through the scan, in place on the pool
+    [slots, H, P, S].  Returns y [B, H, P]."""
+    _need(state_pool, "state_pool", None, 4)
+    _need(state_indices, "state_indices", torch.int32, 1)
+    desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, x.shape[0], state_pool.dtype)
+    _rows(state_pool, "state_pool", 1, (desc.heads, desc.head_dim, desc.state_dim))
+    _rows(state_indices, "state_indices", x.shape[0], ())
+    dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, state_pool, state_indices))
+    desc.num_slots = state_pool.shape[0]
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().kda_ssm_decode(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                    _ptr(dt_bias), _ptr(state_pool), _ptr(state_indices), _ptr(y), _stream(dev)))
+    return y
+
+
+def ssm_decode_multi(x, dt, A_log, B, C, cu_seqlens, state_pool, state_indices, *, D=None, z=None, dt_bias=None,
+                     intermediate_states=None, update_pool=True):
+    """A short run of tokens per request (speculative verify): the state after
+    request n's j-th token goes to intermediate_states[n, j] ([N', steps, H, P,
+    S], rows beyond `steps` not kept), the last one to the pool row with
+    update_pool.  Returns y [T, H, P]."""
+    N = _cu(cu_seqlens)
+    _need(state_pool, "state_pool", None, 4)
+    _need(state_indices, "state_indices", torch.int32, 1)
+    desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, N, state_pool.dtype)
+    one = (desc.heads, desc.head_dim, desc.state_dim)
+    _rows(state_pool, "state_pool", 1, one)
+    _rows(state_indices, "state_indices", N, ())
+    desc.cache_pitch = _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
+    dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, state_pool, state_indices, intermediate_states))
+    desc.num_slots = state_pool.shape[0]
+    desc.cache_steps = 0 if intermediate_states is None else intermediate_states.shape[1]
+    desc.update_pool = 1 if update_pool else 0
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().kda_ssm_decode_multi(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                          _ptr(dt_bias), _ptr(cu_seqlens), _ptr(state_pool), _ptr(state_indices),
+                                          _ptr(intermediate_states) if desc.cache_steps else None, _ptr(y), _stream(dev)))
+    return y
+
+
+def verify_drafts(tokens, target_probs, cu_seqlens, uniform, uniform_next, *, draft_probs=None):
+    """Which drafted tokens stand, and the token after them.  tokens [T] int32
+    are a verify decode's (per request the last accepted token, then its
+    drafts); target_probs [T, V] the target's distribution after each token;
+    draft_probs [T, V] those that token t + 1 was drawn from (None: drafts
+    chosen with certainty); uniform [T] and uniform_next [N] fp32 random
+    numbers in [0, 1).  Draft t + 1 stands while uniform[t] q < p.  Returns
+    (accepted [N], next_tokens [N], emitted [T]), int32: accepted[n] is the
+    step for commit_states and conv_commit (-1: no tokens)."""
+    _need(tokens, "tokens", torch.int32, 1)
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [T, V]")
+    if target_probs.dtype not in _DT:
+        raise ValueError("target_probs must be float32 or bfloat16")
+    N, T, V = _cu(cu_seqlens), tokens.shape[0], target_probs.shape[1]
+    pitch = _token_rows(target_probs, "target_probs", target_probs.dtype, T, (V,))
+    draft_pitch = 0 if draft_probs is None else _token_rows(draft_probs, "draft_probs", target_probs.dtype, T, (V,))
+    _need(uniform, "uniform", torch.float32, 1)
+    _need(uniform_next, "uniform_next", torch.float32, 1)
+    _rows(uniform, "uniform", T, ())
+    _rows(uniform_next, "uniform_next", N, ())
+    dev = _on_device(target_probs, (tokens, cu_seqlens, uniform, uniform_next, draft_probs))
+    desc = VerifyDesc(N, T, V, _DT[target_probs.dtype], pitch, draft_pitch)
+    accepted = torch.empty(N, dtype=torch.int32, device=dev)
+    next_tokens = torch.empty(N, dtype=torch.int32, device=dev)
+    emitted = torch.empty(T, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        nbytes = int(lib().kda_verify_drafts_workspace_size(ctypes.byref(desc)))
+        ws = _scratch(nbytes, dev)
+        _check(lib().kda_verify_drafts(ctypes.byref(desc), _ptr(tokens), _ptr(target_probs), _ptr(draft_probs), _ptr(cu_seqlens),
+                                       _ptr(uniform), _ptr(uniform_next), _ptr(accepted), _ptr(next_tokens), _ptr(emitted), _ptr(ws),
+                                       ws.numel(), _stream(dev)))
+    return accepted, next_tokens, emitted
+
+
+def commit_states(state_pool, state_indices, intermediate_states, steps):
+    """state_pool[state_indices[n]] = intermediate_states[n, steps[n]]: the
+    accepted step of a verify decode's cache becomes the request's state
+    (negative steps, or steps the cache does not hold: left as it is)."""
+    _need(state_pool, "state_pool", None, 4)
+    _need(state_indices, "state_indices", torch.int32, 1)
+    _need(steps, "steps", torch.int32, 1)
+    N = steps.shape[0]
+    _rows(state_pool, "state_pool", 1, tuple(state_pool.shape[1:]))
+    _rows(state_indices, "state_indices", N, ())
+    if intermediate_states is None:
+        raise ValueError("commit_states needs the step cache")
+    pitch = _cache_pitch(intermediate_states, N, *state_pool.shape[1:], state_pool.dtype)
+    dev = _on_device(state_pool, (state_indices, intermediate_states, steps))
+    desc = CommitDesc(N, state_pool.shape[0], intermediate_states.shape[1], pitch,
+                      state_pool[0].numel() * state_pool.element_size())
+    with torch.cuda.device(dev):
+        _check(lib().kda_commit_states(ctypes.byref(desc), _ptr(state_pool), _ptr(state_indices), _ptr(intermediate_states),
+                                       _ptr(steps), _stream(dev)))

@@ -4,7 +4,7 @@
 
 #include <mutex>
 
-#include "../../include/kda.h"
+#include "kda_check.h"
 #include "kda_internal.h"
 
 // Workspace of the allocation-free prefill entry point: one copy of this
@@ -16,18 +16,7 @@ static __device__ __align__(256) unsigned char scratch[KDA_SCRATCH_BYTES];
 
 namespace {
 
-bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
-bool dtype_ok(int t) { return t == KDA_F32 || t == KDA_BF16; }
-bool gate_ok(int t) { return t == KDA_GATE_CHANNEL || t == KDA_GATE_SCALAR; }
-bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t io_size(int t) { return t == KDA_BF16 ? 2 : 4; }
-
-// Byte ranges [p, p + n) overlap?
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
+using namespace kda;
 
 kda_status check_desc(const kda_prefill_desc *d) {
     if (!d) return KDA_ERR_NULL;
@@ -50,8 +39,6 @@ kda_status check_decode_desc(const kda_decode_desc *d) {
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
-
-kda_status hip_status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 // The gate inputs of one call: activated fp32 g and beta, or (raw) the raw
 // projections x, b in the io dtype plus fp32 A_log and dt_bias.
@@ -324,7 +311,7 @@ const char *kda_status_string(kda_status s) {
     return "unknown status";
 }
 
-int32_t kda_version(void) { return 200; }
+int32_t kda_version(void) { return 300; }
 
 size_t kda_chunk_prefill_workspace_size(const kda_prefill_desc *d) {
     if (check_desc(d) != KDA_OK) return 0;

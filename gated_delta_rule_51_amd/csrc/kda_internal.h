@@ -57,4 +57,57 @@ struct PrefillArgs {
 size_t prefill_workspace_bytes(int num_seqs, int total_tokens, int hv, int dk, int dv);
 hipError_t launch_prefill(PrefillArgs &a, void *workspace, hipStream_t stream);
 
+// Short causal convolution.
+struct ConvArgs {
+    const void *x, *weight, *bias;
+    const int32_t *cu_seqlens;
+    const void *state_in;     // dense states, pool, or NULL (zeros)
+    void *state_out;          // dense states, pool, or NULL (not written)
+    const int32_t *indices;   // pool slots or NULL
+    const int32_t *steps;     // commit only
+    void *y;
+    int num_seqs, total_tokens, channels, width, num_slots;
+    bool io_bf16, silu;
+    long x_stride;
+};
+hipError_t launch_conv_prefill(const ConvArgs &a, hipStream_t stream);
+hipError_t launch_conv_decode(const ConvArgs &a, hipStream_t stream);
+hipError_t launch_conv_commit(const ConvArgs &a, hipStream_t stream);
+long conv_prefill_tiles(int num_seqs, int total_tokens);   // workgroup rows of the prefill grid
+
+// Selective state-space scan.
+struct SsmArgs {
+    const void *x, *dt, *B, *C, *z;
+    const float *A_log, *D, *dt_bias;
+    const int32_t *cu_seqlens;   // NULL: one token a request
+    const void *state_in;        // dense states, pool, or NULL (zeros)
+    void *state_out;             // dense states, pool, or NULL (not written)
+    const int32_t *indices;
+    void *cache;                 // step cache or NULL
+    void *y;
+    int num_seqs, total_tokens, heads, groups, p, s, num_slots, cache_steps, cache_pitch;
+    bool io_bf16, state_bf16;
+    long x_stride, dt_stride, b_stride, c_stride, z_stride;
+};
+hipError_t launch_ssm_decode(const SsmArgs &a, hipStream_t stream);
+hipError_t launch_ssm_run(const SsmArgs &a, hipStream_t stream);
+hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t stream);
+size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int p, int s, bool io_bf16);
+
+// Draft verification and commit.
+struct VerifyArgs {
+    const int32_t *tokens, *cu_seqlens;
+    const void *target, *draft;
+    const float *uniform, *uniform_next;
+    int32_t *accepted, *next, *emitted;
+    double *partial;             // [N, 2, parts] sums, or NULL with one part
+    int num_seqs, vocab, parts;
+    bool bf16;
+    long target_stride, draft_stride;
+};
+int verify_parts(int num_seqs, int vocab);
+hipError_t launch_verify(const VerifyArgs &a, hipStream_t stream);
+hipError_t launch_commit(const int32_t *indices, const int32_t *steps, const void *cache, void *pool, int num_seqs,
+                         int num_slots, int cache_steps, int cache_pitch, long row_bytes, hipStream_t stream);
+
 }  // namespace kda

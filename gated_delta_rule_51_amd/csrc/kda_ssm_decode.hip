@@ -1,0 +1,192 @@
+// Selective state-space scan, token by token, against a state pool:
+//     S = exp(-exp(A_log) dt) S + dt x B^T;   y = S C + D x;   y *= silu(z)
+// one token a request (ssm_token_kernel), or a run of tokens with the state in
+// registers (ssm_run_kernel), every state optionally kept in a step cache.
+//
+// As in the delta rule's decode, a workgroup streams BV stored rows (one row
+// per channel p of the head, the S states contiguous) of state[slot, h]; rows
+// are independent given B, C and the step.  Bound by the state's bytes, read
+// once and written once with 16-byte nontemporal accesses.
+#include "kda_device.h"
+#include "kda_internal.h"
+#include "kda_rows.h"
+#include "kda_ssm.h"
+
+namespace kda {
+
+// B and C of one (token, group) for states c0 .. c0+VEC-1, and the step and
+// decay of (token, head).
+template <int VEC, typename IO>
+__device__ __forceinline__ void ssm_inputs(const SsmArgs &a, long t, int h, int g, int c0, float A, float bias,
+                                           float (&Bv)[VEC], float (&Cv)[VEC], float &step, float &dec) {
+    const IO *bp = reinterpret_cast<const IO *>(a.B) + t * a.b_stride + (long)g * a.s + c0;
+    const IO *cp = reinterpret_cast<const IO *>(a.C) + t * a.c_stride + (long)g * a.s + c0;
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+        const f32x4 x = load4(bp + i), y = load4(cp + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            Bv[i + e] = x[e];
+            Cv[i + e] = y[e];
+        }
+    }
+    step = softplus_f(io_traits<IO>::load(reinterpret_cast<const IO *>(a.dt), t * a.dt_stride + h) + bias);
+    dec = exp_f(A * step);
+}
+
+// One token applied to this thread's rows.  x and z are the token's rows of
+// the head; y is stored once every row is done, so that no store waits
+// between two rows' loads.
+template <int DS, int BV, typename IO, typename ST>
+__device__ __forceinline__ void ssm_update(const IO *xp, const IO *zp, IO *yp, float Dh, int r0, int cg,
+                                           float (&s)[RowTile<DS, BV, ST>::NP][RowTile<DS, BV, ST>::VEC],
+                                           const float (&Bv)[RowTile<DS, BV, ST>::VEC],
+                                           const float (&Cv)[RowTile<DS, BV, ST>::VEC], float step, float dec) {
+    using R = RowTile<DS, BV, ST>;
+    float yv[R::NP];
+#pragma unroll
+    for (int p = 0; p < R::NP; ++p) {
+        yv[p] = 0.f;
+        if (row_in<DS, BV, ST>(r0, p)) {
+            const int row = r0 + p * R::RPP;
+            const float x = io_traits<IO>::load(xp, row), u = step * x;
+            float acc = 0.f;
+#pragma unroll
+            for (int i = 0; i < R::VEC; ++i) {
+                s[p][i] = s[p][i] * dec + u * Bv[i];
+                acc += s[p][i] * Cv[i];
+            }
+            yv[p] = group_sum<R::LPR>(acc) + Dh * x;
+            if (zp) {
+                const float z = io_traits<IO>::load(zp, row);
+                yv[p] *= z * sigmoid_f(z);
+            }
+        }
+    }
+    if (cg == 0) {
+#pragma unroll
+        for (int p = 0; p < R::NP; ++p)
+            if (row_in<DS, BV, ST>(r0, p)) io_traits<IO>::store(yp, r0 + p * R::RPP, yv[p]);
+    }
+}
+
+template <int DS, int BV, typename IO, typename ST> __global__ __launch_bounds__(256) void ssm_token_kernel(SsmArgs a) {
+    using R = RowTile<DS, BV, ST>;
+    const int tid = threadIdx.x, cg = tid % R::LPR, r0 = tid / R::LPR;
+    const int nt = a.p / BV;   // row tiles per head
+    const int b = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
+    if (b >= a.num_seqs) return;
+    const int h = (int)blockIdx.x / nt, j0 = ((int)blockIdx.x % nt) * BV;
+    int slot = a.indices[b];
+    if (slot < 0) slot = a.num_slots - 1;
+    ST *st = reinterpret_cast<ST *>(a.state_out) + (((long)slot * a.heads + h) * a.p + j0) * (long)DS;
+    unsigned ro[R::NP];
+    row_offs<DS, BV, ST, true>(r0, cg, ro);
+    float s[R::NP][R::VEC];
+    load_rows<DS, BV, ST, true>(st, ro, r0, s);
+
+    float Bv[R::VEC], Cv[R::VEC], step, dec;
+    ssm_inputs<R::VEC, IO>(a, b, h, h / (a.heads / a.groups), cg * R::VEC, -expf(a.A_log[h]), a.dt_bias ? a.dt_bias[h] : 0.f, Bv,
+                           Cv, step, dec);
+    const long hp = (long)h * a.p + j0;
+    ssm_update<DS, BV, IO, ST>(reinterpret_cast<const IO *>(a.x) + b * a.x_stride + hp,
+                               a.z ? reinterpret_cast<const IO *>(a.z) + b * a.z_stride + hp : nullptr,
+                               reinterpret_cast<IO *>(a.y) + (long)b * a.heads * a.p + hp, a.D ? a.D[h] : 0.f, r0, cg, s, Bv, Cv,
+                               step, dec);
+    store_rows<DS, BV, ST, true>(st, ro, r0, s);
+}
+
+// Request n runs tokens [cu[n], cu[n+1]) from state_in (pool row, dense row or
+// zeros).  Step j's state goes to cache[n * pitch + j] for j < cache_steps, the
+// last one to state_out.
+template <int DS, int BV, typename IO, typename ST> __global__ __launch_bounds__(256) void ssm_run_kernel(SsmArgs a) {
+    using R = RowTile<DS, BV, ST>;
+    const int tid = threadIdx.x, cg = tid % R::LPR, r0 = tid / R::LPR;
+    const int nt = a.p / BV;
+    const int b = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
+    if (b >= a.num_seqs) return;
+    const int h = (int)blockIdx.x / nt, j0 = ((int)blockIdx.x % nt) * BV;
+    const int t0 = a.cu_seqlens[b], t1 = a.cu_seqlens[b + 1];
+    if (t1 <= t0 && (a.indices || !a.state_out)) return;
+    long slot = b;
+    if (a.indices) {
+        slot = a.indices[b];
+        if (slot < 0) slot = a.num_slots - 1;
+    }
+    const long at = ((slot * a.heads + h) * a.p + j0) * (long)DS;
+    unsigned ro[R::NP];
+    row_offs<DS, BV, ST>(r0, cg, ro);
+    float s[R::NP][R::VEC];
+    if (a.state_in) {
+        load_rows<DS, BV, ST, true>(reinterpret_cast<const ST *>(a.state_in) + at, ro, r0, s);
+    } else {
+#pragma unroll
+        for (int p = 0; p < R::NP; ++p)
+#pragma unroll
+            for (int i = 0; i < R::VEC; ++i) s[p][i] = 0.f;
+    }
+
+    if (t1 > t0) {
+        const float A = -expf(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+        const int g = h / (a.heads / a.groups);
+        const long hp = (long)h * a.p + j0, step_elems = (long)a.heads * a.p * DS;
+        float Bv[R::VEC], Cv[R::VEC], step, dec;
+        ssm_inputs<R::VEC, IO>(a, t0, h, g, cg * R::VEC, A, bias, Bv, Cv, step, dec);
+        for (int t = t0; t < t1; ++t) {
+            // the next token's inputs first (the last token reloads itself)
+            float Bn[R::VEC], Cn[R::VEC], step_n, dec_n;
+            ssm_inputs<R::VEC, IO>(a, min(t + 1, t1 - 1), h, g, cg * R::VEC, A, bias, Bn, Cn, step_n, dec_n);
+            ssm_update<DS, BV, IO, ST>(reinterpret_cast<const IO *>(a.x) + t * a.x_stride + hp,
+                                       a.z ? reinterpret_cast<const IO *>(a.z) + t * a.z_stride + hp : nullptr,
+                                       reinterpret_cast<IO *>(a.y) + (long)t * a.heads * a.p + hp, Dh, r0, cg, s, Bv, Cv, step, dec);
+            const int j = t - t0;
+            if (a.cache && j < a.cache_steps) {
+                ST *cb = reinterpret_cast<ST *>(a.cache) + ((long)b * a.cache_pitch + j) * step_elems + hp * DS;
+                const __amdgpu_buffer_rsrc_t cr =
+                    __builtin_amdgcn_make_buffer_rsrc(cb, 0, BV * DS * (int)sizeof(ST), kBufferWord3);
+                store_rows_buf<DS, BV, ST>(cr, ro[0] * (unsigned)sizeof(ST), r0, s);
+            }
+#pragma unroll
+            for (int i = 0; i < R::VEC; ++i) {
+                Bv[i] = Bn[i];
+                Cv[i] = Cn[i];
+            }
+            step = step_n;
+            dec = dec_n;
+        }
+    }
+    if (a.state_out) store_rows<DS, BV, ST, true>(reinterpret_cast<ST *>(a.state_out) + at, ro, r0, s);
+}
+
+template <int DS, int BV, typename IO, typename ST> static hipError_t launch_t(const SsmArgs &a, bool run, hipStream_t stream) {
+    const dim3 grid(a.heads * (a.p / BV), decode_grid_y(a.num_seqs), decode_grid_z(a.num_seqs));
+    if (run) ssm_run_kernel<DS, BV, IO, ST><<<grid, 256, 0, stream>>>(a);
+    else ssm_token_kernel<DS, BV, IO, ST><<<grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+template <int DS, int BV> static hipError_t launch_d(const SsmArgs &a, bool run, hipStream_t s) {
+    if (a.io_bf16) return a.state_bf16 ? launch_t<DS, BV, bf16, bf16>(a, run, s) : launch_t<DS, BV, bf16, float>(a, run, s);
+    return a.state_bf16 ? launch_t<DS, BV, float, bf16>(a, run, s) : launch_t<DS, BV, float, float>(a, run, s);
+}
+template <int DS> static hipError_t launch_b(const SsmArgs &a, bool run, hipStream_t s) {
+    switch (decode_tile(a.p, a.num_seqs, a.heads, run)) {
+    case 32: return launch_d<DS, 32>(a, run, s);
+    case 64: return launch_d<DS, 64>(a, run, s);
+    default: return launch_d<DS, 128>(a, run, s);
+    }
+}
+static hipError_t launch_s(const SsmArgs &a, bool run, hipStream_t s) {
+    switch (a.s) {
+    case 32: return launch_b<32>(a, run, s);
+    case 64: return launch_b<64>(a, run, s);
+    default: return launch_b<128>(a, run, s);
+    }
+}
+
+hipError_t launch_ssm_decode(const SsmArgs &a, hipStream_t s) { return launch_s(a, false, s); }
+hipError_t launch_ssm_run(const SsmArgs &a, hipStream_t s) { return launch_s(a, true, s); }
+
+size_t ssm_prefill_workspace_bytes(int, int, int, int, int, bool) { return 0; }
+hipError_t launch_ssm_prefill(const SsmArgs &a, void *, hipStream_t s) { return launch_ssm_run(a, s); }
+
+}  // namespace kda

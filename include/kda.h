@@ -2,7 +2,10 @@
  * libkda — gated delta rule (Kimi Delta Attention, KDA) on AMD Instinct MI355X
  * (gfx950): chunked prefill over packed variable-length sequences and a
  * one-token recurrent decode, both reading and writing recurrent states
- * either densely or in place in a state pool.
+ * either densely or in place in a state pool.  Beside them the steps a serving
+ * path needs next to them: the short causal convolution, the selective
+ * state-space scan on the same pools, and the verification of drafted tokens
+ * with the commit of the accepted states.
  *
  * The operation (per sequence and value head; S is the K x V state):
  *     S'  = Diag(exp g_t) S          decay, one factor per key channel
@@ -340,6 +343,188 @@ kda_status kda_recurrent_decode_multi_fused_gate(const kda_multi_decode_desc *de
                                                  const int32_t *cu_seqlens,
                                                  void *state_pool, const int32_t *state_indices,
                                                  void *intermediate_states, void *o, void *stream);
+
+/* ---- Short causal convolution ------------------------------------------- */
+
+/* Host-side description of one convolution call. */
+typedef struct {
+    int32_t num_seqs;     /* N >= 0 sequences (or requests, one token each)       */
+    int32_t total_tokens; /* T >= 0, equals cu_seqlens[N] on the device; ignored
+                             by kda_conv_decode                                   */
+    int32_t channels;     /* D > 0, any                                           */
+    int32_t width;        /* taps W in {2, 3, 4}                                  */
+    int32_t io_dtype;     /* kda_dtype of x, weight, bias, the states and y       */
+    int32_t silu;         /* nonzero: y = silu(.), 0: the sum itself              */
+    int32_t num_slots;    /* pool rows (pool mode)                                */
+    int32_t update_pool;  /* pool mode of kda_conv_prefill: nonzero writes the
+                             last inputs back, 0 only reads the pool              */
+    int64_t x_stride;     /* elements between two token rows of x, >= D           */
+} kda_conv_desc;
+
+/*
+ * Depthwise causal convolution over packed sequences, the step in front of
+ * the q, k and v of a delta-rule layer or the x, B and C of a state-space one:
+ *     s[t, c] = bias[c] + sum_{j < W} weight[c, j] x[t - W + 1 + j, c]
+ *     y = silu(s) = s / (1 + e^-s)
+ * with x before a sequence's first token taken from its state, which holds the
+ * last W - 1 raw inputs, oldest first.
+ *   x       [T, D] io dtype, rows x_stride elements apart (a column slice of a
+ *           wider projection is read in place)
+ *   weight  [D, W];  bias [D] or NULL
+ *   state, state_indices, final_state: dense or pool mode as for
+ *           kda_chunk_prefill, a state being [W - 1, D] in the io dtype
+ *           (state NULL = zeros in dense mode).  In pool mode with update_pool
+ *           0 the pool is only read (the verify step of speculative decoding;
+ *           kda_conv_commit then brings the accepted inputs in).
+ *   y       [T, D]; must not overlap any input
+ * Sums are fp32, rounded once to y; the states are copies, exact.  A sequence
+ * of fewer than W - 1 tokens keeps the younger part of its state; an empty one
+ * leaves it as it was (copied to final_state in dense mode).  Rows of x that
+ * are not 16-byte multiples apart, or a D that is no multiple of 16 bytes, run
+ * a narrower kernel.
+ */
+kda_status kda_conv_prefill(const kda_conv_desc *desc, const void *x, const void *weight,
+                            const void *bias, const int32_t *cu_seqlens, void *state,
+                            const int32_t *state_indices, void *final_state, void *y, void *stream);
+
+/* One token of num_seqs requests, in place on the pool [num_slots, W - 1, D]. */
+kda_status kda_conv_decode(const kda_conv_desc *desc, const void *x, const void *weight,
+                           const void *bias, void *state_pool, const int32_t *state_indices, void *y,
+                           void *stream);
+
+/*
+ * After a verify step that only read the pool: request n accepted its tokens
+ * 0 .. steps[n] (steps [N] int32 on the device), so its pool row becomes the
+ * last W - 1 of (the row, then x rows cu_seqlens[n] .. cu_seqlens[n] +
+ * steps[n]).  A step that is negative or not below the request's length
+ * leaves the row as it is.  weight and bias play no part.
+ */
+kda_status kda_conv_commit(const kda_conv_desc *desc, const void *x, const int32_t *cu_seqlens,
+                           const int32_t *steps, void *state_pool, const int32_t *state_indices,
+                           void *stream);
+
+/* ---- Selective state-space scan ------------------------------------------ */
+
+/* Host-side description of one scan call. */
+typedef struct {
+    int32_t num_seqs;     /* N >= 0 sequences or requests                          */
+    int32_t total_tokens; /* T >= 0, equals cu_seqlens[N]; ignored by
+                             kda_ssm_decode                                        */
+    int32_t heads, groups; /* H, G: heads % groups == 0                            */
+    int32_t head_dim;     /* P in {32, 64, 128}                                    */
+    int32_t state_dim;    /* S in {32, 64, 128}                                    */
+    int32_t io_dtype;     /* kda_dtype of x, dt, B, C, z and y                     */
+    int32_t state_dtype;  /* kda_dtype of the states, pools and step caches        */
+    int32_t num_slots;    /* pool rows (pool mode)                                 */
+    int32_t cache_steps;  /* kda_ssm_decode_multi: steps kept per request, or 0    */
+    int32_t cache_pitch;  /* kda_ssm_decode_multi: steps between two requests in
+                             the cache, >= cache_steps                             */
+    int32_t update_pool;  /* kda_ssm_decode_multi: nonzero writes the last state   */
+    int64_t x_stride, dt_stride, b_stride, c_stride, z_stride; /* elements between
+                             two token rows                                        */
+} kda_ssm_desc;
+
+/*
+ * The scan, per sequence and head h (group h / (H / G)), state [P, S]:
+ *     dt    = softplus(dt_raw + dt_bias[h])
+ *     state = exp(-exp(A_log[h]) dt) state + dt x B^T
+ *     y     = state C + D[h] x;   with z:  y = y silu(z)
+ * It is the delta rule's recurrence without the residual, on the same pools:
+ * [slots, H, P, S] is [slots, Hv, V, K].
+ *   x  [T, H, P], dt [T, H], B, C [T, G, S], z [T, H, P] or NULL: io dtype,
+ *      token rows *_stride elements apart, contiguous within a row, so that
+ *      slices of a projection's or a convolution's rows are read in place;
+ *      rows of x, B, C and z lie a multiple of 16 bytes apart
+ *   A_log [H], D [H] or NULL, dt_bias [H] or NULL: fp32
+ *   state, state_indices, final_state, cu_seqlens: as for kda_chunk_prefill
+ *   y  [T, H, P] io dtype, contiguous; must not overlap any input
+ * Precision: fp32 throughout.  Not checked: inputs are finite.
+ */
+size_t kda_ssm_prefill_workspace_size(const kda_ssm_desc *desc);
+kda_status kda_ssm_prefill(const kda_ssm_desc *desc, const void *x, const void *dt,
+                           const float *A_log, const void *B, const void *C, const float *D,
+                           const void *z, const float *dt_bias, const int32_t *cu_seqlens,
+                           void *state, const int32_t *state_indices, void *final_state, void *y,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of num_seqs requests, in place on the pool; all sums in fp32. */
+kda_status kda_ssm_decode(const kda_ssm_desc *desc, const void *x, const void *dt,
+                          const float *A_log, const void *B, const void *C, const float *D,
+                          const void *z, const float *dt_bias, void *state_pool,
+                          const int32_t *state_indices, void *y, void *stream);
+
+/*
+ * A short run of tokens per request (speculative verify), with the state after
+ * step j kept at intermediate_states[n * cache_pitch + j] for j < cache_steps
+ * (NULL when cache_steps is 0), as for kda_recurrent_decode_multi.
+ */
+kda_status kda_ssm_decode_multi(const kda_ssm_desc *desc, const void *x, const void *dt,
+                                const float *A_log, const void *B, const void *C, const float *D,
+                                const void *z, const float *dt_bias, const int32_t *cu_seqlens,
+                                void *state_pool, const int32_t *state_indices,
+                                void *intermediate_states, void *y, void *stream);
+
+/* ---- Speculative decoding: which drafts stand, and their states ----------- */
+
+typedef struct {
+    int32_t num_seqs;     /* N >= 0 requests                                       */
+    int32_t total_tokens; /* T >= 0, equals cu_seqlens[N]                          */
+    int32_t vocab;        /* V > 0                                                 */
+    int32_t prob_dtype;   /* kda_dtype of the probabilities                        */
+    int64_t target_stride, draft_stride; /* elements between two rows, >= V        */
+} kda_verify_desc;
+
+/*
+ * Verification of drafted tokens against the target's probabilities.  Request
+ * n's tokens cu_seqlens[n] .. cu_seqlens[n+1] - 1 are those of the verify
+ * decode: first the last accepted token, then its drafts.  Row t of
+ * target_probs is the target's distribution after token t, row t of
+ * draft_probs the one that draft t + 1 was drawn from (NULL: the drafts were
+ * chosen with certainty, q = 1 at the draft).  With d = tokens[t + 1]:
+ *     draft t + 1 stands while  uniform[t] * q_t(d) < p_t(d)   (fp32)
+ * and the first that does not ends the run.  The next token is the first i
+ * with  cum_i > uniform_next[n] * cum_{V-1},  cum the running sums of
+ * max(p - q, 0) at the refused row (of p without d for certain drafts; of p
+ * itself where that leaves nothing), of p after the last token where every
+ * draft stood.
+ *   tokens  [T] int32;  target_probs, draft_probs [T, V] prob dtype
+ *   uniform [T], uniform_next [N] fp32 in [0, 1)
+ *   accepted    [N] int32: how many drafts stood, the step whose state
+ *               kda_commit_states takes; -1 for a request with no tokens
+ *   next_tokens [N] int32: the token after them; -1 where no probability is
+ *               above zero, or for a request with no tokens
+ *   emitted     [T] int32, in the request's rows: the drafts that stood, the
+ *               next token, then -1
+ * The running sums are formed in fp64, so the token found does not depend on
+ * how they are split.  A draft outside [0, V) is refused, without a read, and
+ * takes no weight from its row.  Probabilities that are NaN or not above zero
+ * weigh nothing.  Outputs overlap no input and not one another.
+ */
+size_t kda_verify_drafts_workspace_size(const kda_verify_desc *desc);
+kda_status kda_verify_drafts(const kda_verify_desc *desc, const int32_t *tokens,
+                             const void *target_probs, const void *draft_probs,
+                             const int32_t *cu_seqlens, const float *uniform,
+                             const float *uniform_next, int32_t *accepted, int32_t *next_tokens,
+                             int32_t *emitted, void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct {
+    int32_t num_seqs;     /* N >= 0 requests                                       */
+    int32_t num_slots;    /* pool rows                                             */
+    int32_t cache_steps;  /* steps kept per request                                */
+    int32_t cache_pitch;  /* steps between two requests in the cache               */
+    int64_t row_bytes;    /* bytes of one state of all heads, a multiple of 16     */
+} kda_commit_desc;
+
+/*
+ * pool[slot(n)] = intermediate_states[n * cache_pitch + steps[n]]: the state
+ * after the accepted step of a verify decode (of either kind) becomes the
+ * request's state.  steps [N] int32 on the device; a step that is negative or
+ * not below cache_steps leaves the pool row as it is.  The cache and the pool
+ * must not overlap.
+ */
+kda_status kda_commit_states(const kda_commit_desc *desc, void *state_pool,
+                             const int32_t *state_indices, const void *intermediate_states,
+                             const int32_t *steps, void *stream);
 
 /* Static description of a status code. */
 const char *kda_status_string(kda_status status);

@@ -1,0 +1,215 @@
+"""Convolution, scan, verification and commit entry points without a GPU: the
+descriptors' layouts, and every refusal that host-visible values decide, through
+the C ABI (fake, never dereferenced addresses) and through the binding."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import gated_delta_rule_51_amd as kda
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, NULL, SHAPE, UNSUP, WS, ALIAS, HIP, ALIGN = range(8)
+BASE = 1 << 40
+
+
+def fake(i, off=0):
+    return BASE + i * (1 << 36) + off
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(kda.library_path()):
+        from gated_delta_rule_51_amd import build
+        build.build()
+    return kda.lib()
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
+def test_descriptor_layouts(tmp_path):
+    structs = {"kda_conv_desc": kda.ConvDesc, "kda_ssm_desc": kda.SsmDesc, "kda_verify_desc": kda.VerifyDesc,
+               "kda_commit_desc": kda.CommitDesc}
+    lines = ["#include <stddef.h>", "#include <stdio.h>", '#include "kda.h"', "int main(void) {"]
+    for c, ct in structs.items():
+        lines.append('    printf("%s %%zu\\n", sizeof(%s));' % (c, c))
+        lines += ['    printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (c, f, c, f) for f, _ in ct._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("\n".join(lines + ["    return 0;", "}"]) + "\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = dict(line.rsplit(" ", 1) for line in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines())
+    for c, ct in structs.items():
+        assert int(got[c]) == ctypes.sizeof(ct)
+        for f, _ in ct._fields_:
+            assert int(got["%s.%s" % (c, f)]) == getattr(ct, f).offset, (c, f)
+
+
+def conv_desc(**kw):
+    d = dict(num_seqs=3, total_tokens=20, channels=64, width=4, io_dtype=1, silu=1, num_slots=8, update_pool=1, x_stride=64)
+    d.update(kw)
+    return kda.ConvDesc(**d)
+
+
+def conv(L, d, **kw):
+    a = dict(x=fake(1), w=fake(2), b=fake(3), cu=fake(4), state=None, idx=None, final=fake(5), y=fake(6))
+    a.update(kw)
+    return L.kda_conv_prefill(ctypes.byref(d), a["x"], a["w"], a["b"], a["cu"], a["state"], a["idx"], a["final"], a["y"], None)
+
+
+def test_conv_refusals(L):
+    assert L.kda_conv_prefill(None, *[None] * 9) == NULL
+    for kw, want in ((dict(width=1), UNSUP), (dict(width=5), UNSUP), (dict(io_dtype=2), UNSUP), (dict(channels=0), SHAPE),
+                     (dict(x_stride=63), SHAPE), (dict(num_seqs=-1), SHAPE), (dict(total_tokens=-1), SHAPE)):
+        assert conv(L, conv_desc(**kw)) == want, kw
+    d = conv_desc()
+    for kw, want in ((dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL), (dict(cu=None), NULL),
+                     (dict(x=fake(1, 2)), ALIGN), (dict(y=fake(1, 64)), ALIAS), (dict(final=fake(6, 128)), ALIAS),
+                     (dict(idx=fake(7)), NULL), (dict(idx=fake(7), state=fake(8)), ALIAS),
+                     (dict(idx=fake(7), state=fake(8), final=None, y=fake(8, 64)), ALIAS)):
+        assert conv(L, d, **kw) == want, kw
+    assert conv(L, conv_desc(num_slots=0), idx=fake(7), state=fake(8), final=None) == SHAPE
+    assert conv(L, conv_desc(num_seqs=0, total_tokens=0)) == OK
+    dec = lambda d, x=fake(1), y=fake(6), pool=fake(8), idx=fake(7): L.kda_conv_decode(  # noqa: E731
+        ctypes.byref(d), x, fake(2), fake(3), pool, idx, y, None)
+    assert dec(conv_desc(num_seqs=0), x=None) == OK
+    assert dec(d, pool=None) == NULL and dec(d, idx=None) == NULL and dec(d, y=fake(8)) == ALIAS
+    assert dec(d, x=fake(8, 64)) == ALIAS and dec(conv_desc(num_slots=0)) == SHAPE
+    com = lambda d, x=fake(1), steps=fake(9): L.kda_conv_commit(ctypes.byref(d), x, fake(4), steps, fake(8), fake(7), None)  # noqa: E731
+    assert com(d, steps=None) == NULL and com(d, x=fake(8)) == ALIAS and com(conv_desc(width=7)) == UNSUP
+    assert com(conv_desc(total_tokens=0), x=None) == OK
+
+
+def ssm_desc(**kw):
+    d = dict(num_seqs=3, total_tokens=20, heads=4, groups=2, head_dim=64, state_dim=128, io_dtype=1, state_dtype=0, num_slots=8,
+             cache_steps=0, cache_pitch=0, update_pool=1, x_stride=256, dt_stride=4, b_stride=256, c_stride=256, z_stride=256)
+    d.update(kw)
+    return kda.SsmDesc(**d)
+
+
+def ssm(L, d, **kw):
+    a = dict(x=fake(1), dt=fake(2), A=fake(3), B=fake(4), C=fake(5), D=fake(6), z=fake(7), bias=fake(8), cu=fake(9), state=None,
+             idx=None, final=fake(10), y=fake(11), ws=fake(12), n=1 << 34)
+    a.update(kw)
+    return L.kda_ssm_prefill(ctypes.byref(d), *(a[k] for k in ("x", "dt", "A", "B", "C", "D", "z", "bias", "cu", "state", "idx",
+                                                               "final", "y", "ws", "n")), None)
+
+
+def test_ssm_refusals(L):
+    assert L.kda_ssm_prefill(None, *[None] * 14, 0, None) == NULL
+    assert L.kda_ssm_prefill_workspace_size(None) == 0
+    assert L.kda_ssm_prefill_workspace_size(ctypes.byref(ssm_desc(head_dim=48))) == 0
+    for kw, want in ((dict(heads=3), SHAPE), (dict(groups=0), SHAPE), (dict(head_dim=96), UNSUP), (dict(state_dim=16), UNSUP),
+                     (dict(io_dtype=3), UNSUP), (dict(state_dtype=-1), UNSUP), (dict(x_stride=255), SHAPE), (dict(dt_stride=3), SHAPE),
+                     (dict(b_stride=8), SHAPE), (dict(c_stride=8), SHAPE), (dict(z_stride=8), SHAPE), (dict(x_stride=260), ALIGN),
+                     (dict(b_stride=258), ALIGN), (dict(c_stride=257), ALIGN), (dict(z_stride=257), ALIGN)):
+        assert ssm(L, ssm_desc(**kw)) == want, kw
+    d = ssm_desc()
+    for kw, want in ((dict(x=None), NULL), (dict(dt=None), NULL), (dict(A=None), NULL), (dict(B=None), NULL), (dict(C=None), NULL),
+                     (dict(y=None), NULL), (dict(cu=None), NULL), (dict(x=fake(1, 8)), ALIGN), (dict(D=fake(6, 4)), ALIGN),
+                     (dict(y=fake(1, 1024)), ALIAS), (dict(y=fake(7)), ALIAS), (dict(final=fake(4)), ALIAS), (dict(y=fake(10)), ALIAS),
+                     (dict(idx=fake(13)), NULL), (dict(idx=fake(13), state=fake(14)), ALIAS),
+                     (dict(idx=fake(13), state=fake(14), final=None, y=fake(14, 64)), ALIAS)):
+        assert ssm(L, d, **kw) == want, kw
+    assert ssm(L, ssm_desc(num_seqs=0, total_tokens=0)) == OK
+    args = [fake(i) for i in range(1, 9)]
+    dec = lambda d, pool=fake(14), idx=fake(13), y=fake(11): L.kda_ssm_decode(ctypes.byref(d), *args, pool, idx, y, None)  # noqa: E731
+    assert dec(d, pool=None) == NULL and dec(d, idx=None) == NULL and dec(d, y=fake(14, 256)) == ALIAS
+    assert dec(ssm_desc(num_slots=0)) == SHAPE and dec(ssm_desc(num_seqs=0), pool=None) == OK
+    multi = lambda d, cu=fake(9), cache=fake(15), y=fake(11): L.kda_ssm_decode_multi(  # noqa: E731
+        ctypes.byref(d), *args, cu, fake(14), fake(13), cache, y, None)
+    k = ssm_desc(cache_steps=2, cache_pitch=4)
+    assert multi(k, cu=None) == NULL and multi(k, cache=None) == NULL and multi(k, cache=fake(14, 4096)) == ALIAS
+    assert multi(k, cache=fake(15, 4)) == ALIGN and multi(k, y=fake(15)) == ALIAS
+    assert multi(ssm_desc(cache_steps=5, cache_pitch=4)) == SHAPE and multi(ssm_desc(total_tokens=0), cache=None) == OK
+
+
+def test_verify_refusals(L):
+    def desc(**kw):
+        d = dict(num_seqs=3, total_tokens=9, vocab=100, prob_dtype=0, target_stride=100, draft_stride=100)
+        d.update(kw)
+        return kda.VerifyDesc(**d)
+
+    def call(d, **kw):
+        a = dict(tok=fake(1), p=fake(2), q=fake(3), cu=fake(4), u=fake(5), r=fake(6), acc=fake(7), nxt=fake(8), out=fake(9),
+                 ws=fake(10), n=1 << 30)
+        a.update(kw)
+        return L.kda_verify_drafts(ctypes.byref(d), *a.values(), None)
+
+    assert L.kda_verify_drafts_workspace_size(None) == 0 and L.kda_verify_drafts_workspace_size(ctypes.byref(desc())) > 0
+    assert L.kda_verify_drafts(None, *[None] * 10, 0, None) == NULL
+    for kw, want in ((dict(vocab=0), SHAPE), (dict(target_stride=99), SHAPE), (dict(draft_stride=99), SHAPE), (dict(prob_dtype=2), UNSUP),
+                     (dict(num_seqs=-1), SHAPE), (dict(vocab=(1 << 30) + 1, target_stride=1 << 31), UNSUP)):
+        assert call(desc(**kw)) == want, kw
+    for kw, want in ((dict(tok=None), NULL), (dict(p=None), NULL), (dict(cu=None), NULL), (dict(u=None), NULL), (dict(r=None), NULL),
+                     (dict(acc=None), NULL), (dict(nxt=None), NULL), (dict(out=None), NULL), (dict(p=fake(2, 4)), ALIGN),
+                     (dict(ws=None), WS), (dict(n=16), WS), (dict(out=fake(1)), ALIAS), (dict(acc=fake(8)), ALIAS),
+                     (dict(ws=fake(2, 64)), ALIAS)):
+        assert call(desc(), **kw) == want, kw
+    assert call(desc(num_seqs=0, total_tokens=0), tok=None) == OK
+
+
+def test_commit_refusals(L):
+    def call(pool=fake(1), idx=fake(2), cache=fake(3), steps=fake(4), **kw):
+        d = dict(num_seqs=3, num_slots=8, cache_steps=4, cache_pitch=4, row_bytes=4096)
+        d.update(kw)
+        return L.kda_commit_states(ctypes.byref(kda.CommitDesc(**d)), pool, idx, cache, steps, None)
+
+    assert L.kda_commit_states(None, *[None] * 5) == NULL
+    assert call(pool=None) == NULL and call(steps=None) == NULL and call(cache=None) == NULL and call(idx=None) == NULL
+    assert call(row_bytes=24) == SHAPE and call(row_bytes=0) == SHAPE and call(cache_pitch=3) == SHAPE and call(num_slots=0) == SHAPE
+    assert call(cache=fake(1, 8192)) == ALIAS and call(cache=fake(3, 8)) == ALIGN
+    assert call(num_seqs=0, pool=None) == OK and call(cache_steps=0, cache=None) == OK
+
+
+def test_binding_refusals():
+    bf, i32 = torch.bfloat16, torch.int32
+    z = torch.zeros
+    cu, idx = torch.tensor([0, 4, 10], dtype=i32), z(2, dtype=i32)
+    x, w = z(10, 64, dtype=bf), z(64, 4, dtype=bf)
+    pool = z(5, 3, 64, dtype=bf)
+    X, dt, A, B = z(10, 4, 32, dtype=bf), z(10, 4, dtype=bf), z(4), z(10, 2, 64, dtype=bf)
+    S = z(5, 4, 32, 64)
+    p, tok, u, r = z(10, 50), z(10, dtype=i32), z(10), z(2)
+    steps = z(2, dtype=i32)
+    bad = [
+        (lambda: kda.conv_prefill(x, w[:32], None, cu), "weight must have shape"),
+        (lambda: kda.conv_prefill(x, w.float(), None, cu), "weight must be"),
+        (lambda: kda.conv_prefill(x.half(), w.half(), None, cu), "float32 or bfloat16"),
+        (lambda: kda.conv_prefill(x.t().contiguous().t(), w, None, cu), "contiguous within a row"),
+        (lambda: kda.conv_prefill(x, w, None, cu, state_indices=idx), "pool mode needs"),
+        (lambda: kda.conv_prefill(x, w, None, cu, initial_state=pool[:1], state_indices=None), "initial_state must have shape"),
+        (lambda: kda.conv_prefill(x, w, None, cu, initial_state=pool[:, :2].contiguous(), state_indices=idx), "state pool must have shape"),
+        (lambda: kda.conv_prefill(x, w, None, cu, activation="relu"), "activation"),
+        (lambda: kda.conv_prefill(x[:1].expand(10, 64), w, None, cu), "overlap"),
+        (lambda: kda.conv_decode(x, w, None, pool, idx), "state_indices must have shape"),
+        (lambda: kda.conv_commit(x, cu, steps[:1], pool, idx), "steps must have shape"),
+        (lambda: kda.ssm_prefill(X, dt[:, :3], A, B, B, cu), "dt must have shape"),
+        (lambda: kda.ssm_prefill(X, dt, A[:3], B, B, cu), "A_log must have shape"),
+        (lambda: kda.ssm_prefill(X, dt, A, B, B[:, :1], cu), "C must have shape"),
+        (lambda: kda.ssm_prefill(X, dt, A, z(10, 3, 64, dtype=bf), z(10, 3, 64, dtype=bf), cu), "multiple of groups"),
+        (lambda: kda.ssm_prefill(X, dt, A, B, B, cu, z=X.float()), "z must be"),
+        (lambda: kda.ssm_prefill(X, dt, A, B, B, cu, initial_state=S.transpose(2, 3).contiguous(), state_indices=idx), "state pool"),
+        (lambda: kda.ssm_prefill(X, dt, A, B, B, cu, initial_state=S[:1]), "initial_state must have shape"),
+        (lambda: kda.ssm_prefill(X, dt, A, B, B, cu, initial_state=S.double()), "float32 or bfloat16"),
+        (lambda: kda.ssm_decode(X, dt, A, B, B, S, idx), "state_indices must have shape"),
+        (lambda: kda.ssm_decode_multi(X, dt, A, B, B, cu, S, idx, intermediate_states=z(1, 4, 4, 32, 64)), "intermediate_states"),
+        (lambda: kda.verify_drafts(tok, p[:9], cu, u, r), "target_probs must have shape"),
+        (lambda: kda.verify_drafts(tok, p, cu, u[:3], r), "uniform must have shape"),
+        (lambda: kda.verify_drafts(tok, p, cu, u, r[:1]), "uniform_next must have shape"),
+        (lambda: kda.verify_drafts(tok, p, cu, u, r, draft_probs=p.to(bf)), "draft_probs must be"),
+        (lambda: kda.verify_drafts(tok.long(), p, cu, u, r), "tokens must be"),
+        (lambda: kda.commit_states(S, idx, z(2, 3, 4, 32, 32), steps), "intermediate_states"),
+        (lambda: kda.commit_states(S, idx, z(2, 3, 4, 32, 64, dtype=bf), steps), "intermediate_states"),
+    ]
+    host = [
+        lambda: kda.conv_prefill(x, w, None, cu), lambda: kda.conv_decode(x[:2], w, None, pool, idx),
+        lambda: kda.conv_commit(x, cu, steps, pool, idx), lambda: kda.ssm_prefill(X, dt, A, B, B, cu),
+        lambda: kda.ssm_decode(X[:2], dt[:2], A, B[:2], B[:2], S, idx), lambda: kda.ssm_decode_multi(X, dt, A, B, B, cu, S, idx),
+        lambda: kda.verify_drafts(tok, p, cu, u, r), lambda: kda.commit_states(S, idx, z(2, 3, 4, 32, 64), steps),
+    ]
+    for call, msg in bad + [(c, "GPU tensors") for c in host]:
+        with pytest.raises(ValueError, match=msg):
+            call()
