@@ -78,6 +78,9 @@ kda_status check_ssm(const kda_ssm_desc *d, bool pool) {
         return KDA_ERR_UNSUPPORTED;
     const long hp = (long)d->heads * d->head_dim, gs = (long)d->groups * d->state_dim;
     if (d->x_stride < hp || d->dt_stride < d->heads || d->b_stride < gs || d->c_stride < gs || d->z_stride < 0) return KDA_ERR_SHAPE;
+    // 64 rows stay within a buffer resource's 31 bits
+    const int64_t far = 1 << 23;
+    if (d->x_stride > far || d->b_stride > far || d->c_stride > far) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -186,7 +186,4 @@ static hipError_t launch_s(const SsmArgs &a, bool run, hipStream_t s) {
 hipError_t launch_ssm_decode(const SsmArgs &a, hipStream_t s) { return launch_s(a, false, s); }
 hipError_t launch_ssm_run(const SsmArgs &a, hipStream_t s) { return launch_s(a, true, s); }
 
-size_t ssm_prefill_workspace_bytes(int, int, int, int, int, bool) { return 0; }
-hipError_t launch_ssm_prefill(const SsmArgs &a, void *, hipStream_t s) { return launch_ssm_run(a, s); }
-
 }  // namespace kda
