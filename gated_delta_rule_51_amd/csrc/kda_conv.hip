@@ -17,9 +17,6 @@ namespace kda {
 // again (3 of 35 at four taps, from the caches).
 constexpr int kConvTile = 32;
 
-// Sequence n's tiles take the slots floor(cu[n] / R) + n onwards: at least
-// ceil(L / R) of them lie before the next sequence's first, one where L is 0,
-// so the tile a slot stands for is found by a search in cu_seqlens alone.
 long conv_prefill_tiles(int num_seqs, int total_tokens) {
     return num_seqs <= 0 ? 0 : (long)total_tokens / kConvTile + num_seqs;
 }
@@ -83,14 +80,8 @@ template <typename IO, int VEC, int W> __global__ __launch_bounds__(256) void co
     const int slot = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
     const int c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * VEC;
     if (slot >= slots) return;
-    // the last n with floor(cu[n] / R) + n <= slot
-    int lo = 0, hi = a.num_seqs - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu_seqlens[mid] / kConvTile + mid <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    const int n = lo, begin = a.cu_seqlens[n], len = a.cu_seqlens[n + 1] - begin;
+    const int n = slot_sequence(a.cu_seqlens, a.num_seqs, slot, kConvTile);
+    const int begin = a.cu_seqlens[n], len = a.cu_seqlens[n + 1] - begin;
     const int local = (slot - (begin / kConvTile + n)) * kConvTile;   // first token of the tile
     if (c >= a.channels || (local >= len && local > 0)) return;
 

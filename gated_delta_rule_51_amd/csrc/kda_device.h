@@ -83,6 +83,24 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return (uint32_t)f32_to_bf16(lo) | ((uint32_t)f32_to_bf16(hi) << 16);
 }
 
+// The sequence whose tiles of R tokens hold `slot`, where sequence n's tiles
+// take the slots floor(cu[n] / R) + n onwards: at least ceil(L / R) of them lie
+// before the next sequence's first (one where L is 0), so cu_seqlens alone
+// tells what a slot stands for, and floor(T / R) + N slots hold every tile.
+// The whole wave searches, 64 ways a step.
+__device__ __forceinline__ int slot_sequence(const int32_t *cu, int num_seqs, int slot, int R) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = num_seqs;
+    while (n > 1) {
+        const int step = (n + 63) / 64, i = lane * step;
+        const unsigned long long m = __ballot(i < n && cu[lo + min(i, n - 1)] / R + lo + i <= slot);
+        const int k = (63 - __builtin_clzll(m | 1)) * step;
+        lo += k;
+        n = min(step, n - k);
+    }
+    return lo;
+}
+
 template <int W> __device__ __forceinline__ float group_sum(float x) {
     // Sum over W consecutive lanes (W a power of two <= 64).
 #pragma unroll

@@ -219,7 +219,7 @@ kda_status kda_conv_commit(const kda_conv_desc *d, const void *x, const int32_t 
 
 size_t kda_ssm_prefill_workspace_size(const kda_ssm_desc *d) {
     if (check_ssm(d, false) != KDA_OK) return 0;
-    return ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->head_dim, d->state_dim,
+    return ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim, d->state_dim,
                                        d->io_dtype == KDA_BF16);
 }
 
@@ -233,7 +233,7 @@ kda_status kda_ssm_prefill(const kda_ssm_desc *d, const void *x, const void *dt,
     const long T = d->total_tokens, N = d->num_seqs;
     if (!cu_seqlens || (pool && !state)) return KDA_ERR_NULL;
     if (pool && final_state && final_state != state) return KDA_ERR_ALIAS;
-    const size_t need = ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->head_dim, d->state_dim,
+    const size_t need = ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim, d->state_dim,
                                                     d->io_dtype == KDA_BF16);
     const Range before{state, ssm_states(d, pool ? d->num_slots : N)}, last{pool ? nullptr : final_state, ssm_states(d, N)};
     const Range more[5] = {before, last, {cu_seqlens, (size_t)(N + 1) * 4}, {state_indices, (size_t)N * 4}, {workspace, need}};

@@ -10,4 +10,10 @@ namespace kda {
 // rounded to fp32 first would lose 6e-5 of a step of 1e-3.
 __device__ __forceinline__ float softplus_f(float z) { return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))); }
 
+// Two floats rounded to bf16 in one instruction.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 }  // namespace kda

@@ -25,6 +25,16 @@
 // states keep fp32's accuracy, in the whole range of bf16.  The sums G are
 // formed in fp64 and kept as two floats: differences of large sums would
 // otherwise lose the small decays between neighbours.
+//
+// Segments.  A chain of chunks is latency bound, and few long sequences leave
+// the chip idle, so sequences are cut into segments.  The first launch runs
+// every sequence's first segment whole, the second the states alone of those
+// between the first and the last, from zero; a third carries the states across
+// them (state = decay of the segment x the state before it + its own); the last
+// runs the other segments whole, each from the state before it.  Sequences of
+// one or two segments thus do no work twice.
+#include <type_traits>
+
 #include "kda_device.h"
 #include "kda_internal.h"
 #include "kda_ssm.h"
@@ -56,7 +66,7 @@ template <int TERMS> __device__ __forceinline__ void split(const float (&v)[8], 
         float x = v[2 * i], y = v[2 * i + 1];
 #pragma unroll
         for (int k = 0; k < TERMS; ++k) {
-            const uint32_t w = pack_bf16x2(x, y);
+            const uint32_t w = pack2(x, y);
             t[k][i] = w;
             if (k + 1 < TERMS) {
                 x -= lo_f(w);
@@ -66,64 +76,104 @@ template <int TERMS> __device__ __forceinline__ void split(const float (&v)[8], 
     }
 }
 
-constexpr int kGateArrays = 5;   // G (two floats), dt, exp(G_last - G) dt, exp(G)
+// A value (of 8 bytes) all lanes share, in scalar registers.
+template <typename T> __device__ __forceinline__ T uniform(T x) {
+    static_assert(sizeof(T) == 8, "two registers");
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(T, u32x2{(uint32_t)__builtin_amdgcn_readfirstlane((int)w[0]),
+                                       (uint32_t)__builtin_amdgcn_readfirstlane((int)w[1])});
+}
+
+// Per token of a chunk: 0 and 1 the two floats of G (in powers of 2), 2 dt
+// over the decay of the second, 3 exp(G_last - G) dt, 4 exp(G).
+constexpr int kGateArrays = 5;
 
 template <int P, int S> struct Chunk {
     static constexpr int WPH = P / 32;          // waves of a head
     static constexpr int HW = 4 / WPH;          // heads of a workgroup
     static constexpr int NT = S / 32;           // 32-wide tiles of the state's columns
-    static constexpr int XROW = 256 + 32;       // LDS row strides: 32 bytes past the row keep
-    static constexpr int BROW = 2 * S + 32;     // both kinds of reads free of bank conflicts
     static constexpr int PPR = S / 8;           // 16-byte pieces of a row of B
     static constexpr int PB = PPR / 4;          // pieces of B a thread stages
     static constexpr int MBYTES = WPH == 1 ? 0 : 3 * 2 * 2 * 1024;   // M of one head
-    static constexpr int OFF_B = 64 * XROW, OFF_C = OFF_B + 64 * BROW, OFF_M = OFF_C + 64 * BROW;
+    static constexpr int OFF_B = 64 * 256, OFF_C = OFF_B + 64 * 2 * S, OFF_M = OFF_C + 64 * 2 * S;
     static constexpr int OFF_G = OFF_M + HW * MBYTES;
     static constexpr int GBYTES = HW * kGateArrays * 256;            // one buffer of gates
     static constexpr int LDS = OFF_G + 2 * GBYTES;
 };
 
-// M's tile (rows t of 32 tt, columns s of 32 ss) from the products C_t . B_s,
-// as two operands of 16 tokens each in two bf16 terms.
-__device__ __forceinline__ void m_tile(const f32x16 &cb, const float *gate, int tt, int ss, int lane, float Dh, u32x4 (&m)[2][2]) {
-    const int t = 32 * tt + (lane & 31), hh = lane >> 5;
-    const float gt = gate[t], lt = gate[64 + t];
+// Byte offset of a row's 16-byte piece in an LDS tile of PPR pieces a row.
+// Pieces are exchanged within rows so that neither 16 rows of one piece (the
+// operands' own order) nor four rows of two neighbours (the transposed reads)
+// meet in a bank.
+template <int PPR> __device__ __forceinline__ int swizzle(int row) {
+    const int q2 = row / (16 / PPR) * 2;
+    return (q2 & (PPR - 1)) | ((q2 / PPR) & 1);
+}
+template <int PPR> __device__ __forceinline__ int tile_at(int row, int piece) {
+    return row * PPR * 16 + ((piece ^ swizzle<PPR>(row & 15)) << 4);   // repeats every 16 rows
+}
+
+// Four columns of M's tile (rows t of 32 tt, columns s of 32 ss) from the
+// products C_t . B_s: registers 4q .. 4q + 3.  Every pair has its own
+// exponential, as a factor to a common point would overflow.
+__device__ __forceinline__ void m_part(const f32x16 &cb, const float *gate, int tt, int ss, int q, int lane, float Dh, float gt,
+                                       float lt, float (&v)[4]) {
+    const int t = 32 * tt + (lane & 31), s0 = 32 * ss + 8 * q + 4 * (lane >> 5);
+    const f32x4 gs = *reinterpret_cast<const f32x4 *>(gate + s0), ds = *reinterpret_cast<const f32x4 *>(gate + 128 + s0);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int s0 = 32 * ss + 8 * (2 * u + k) + 4 * hh;
-            const f32x4 gs = *reinterpret_cast<const f32x4 *>(gate + s0), ls = *reinterpret_cast<const f32x4 *>(gate + 64 + s0);
-            const f32x4 ds = *reinterpret_cast<const f32x4 *>(gate + 128 + s0);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const float e = __builtin_amdgcn_exp2f((gt - gs[b]) + (lt - ls[b])) * ds[b];
-                float x = cb[4 * (2 * u + k) + b] * e;
-                if (tt == ss) {
-                    x = s0 + b == t ? x + Dh : x;
-                    x = s0 + b <= t ? x : 0.f;
-                }
-                v[4 * k + b] = x;
-            }
-        }
-        split<2>(v, m[u]);
+    for (int b = 0; b < 4; ++b) {
+        float x = cb[4 * q + b] * (__builtin_amdgcn_exp2f((gt - gs[b]) + lt) * ds[b]);
+        x = s0 + b == t ? x + Dh : x;
+        v[b] = s0 + b <= t ? x : 0.f;
     }
 }
 
-template <int P, int S, typename ST> __global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmArgs a) {
+// Inclusive sums over the wave's lanes, without a trip through LDS.
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_add(double x) {
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return x + __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xf, false),
+                                                (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xf, false)});
+}
+__device__ __forceinline__ double wave_scan(double x) {
+    x = dpp_add<0x111, 0xf>(x);   // from 1, 2, 4 and 8 lanes below within a row of 16
+    x = dpp_add<0x112, 0xf>(x);
+    x = dpp_add<0x114, 0xf>(x);
+    x = dpp_add<0x118, 0xf>(x);
+    x = dpp_add<0x142, 0xa>(x);   // a row's last lane to the next row
+    return dpp_add<0x143, 0xc>(x);   // lane 31 to the upper half
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)w[0], lane),
+                                            (uint32_t)__builtin_amdgcn_readlane((int)w[1], lane)});
+}
+
+struct Segments {
+    int len;        // tokens, a multiple of 64
+    int slots;      // floor(T / len) + N
+    bool later;     // the last launch
+    float *states;  // [slots, H, P, S]: after the segment; before the next one once carried
+    float *decays;  // [slots, H]
+};
+
+template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmArgs a, Segments sg) {
     using C = Chunk<P, S>;
     extern __shared__ __align__(16) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int hh = lane >> 5, l32 = lane & 31;
     const int hs = wave / C::WPH, pc = wave % C::WPH;   // head of the workgroup, 32-column block of the head
 
     const int rep = a.heads / a.groups, blocks = (rep + C::HW - 1) / C::HW;
-    const int seq = (int)blockIdx.x / (a.groups * blocks), rest = (int)blockIdx.x % (a.groups * blocks);
+    const int sl = (int)blockIdx.x / (a.groups * blocks), rest = (int)blockIdx.x % (a.groups * blocks);
     const int g = rest / blocks, first = g * rep + rest % blocks * C::HW;   // first head
     const int h = first + hs;
     const bool active = h < (g + 1) * rep;
-    const int t0 = a.cu_seqlens[seq], len = a.cu_seqlens[seq + 1] - t0;
+    const int seq = __builtin_amdgcn_readfirstlane(sg.slots == a.num_seqs ? sl : slot_sequence(a.cu_seqlens, a.num_seqs, sl, sg.len));
+    const int begin = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq]);
+    const int whole = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq + 1]) - begin;
+    const int local = sg.slots == a.num_seqs ? 0 : sl - (begin / sg.len + seq);   // segment of the sequence
+    const int segs = max(1, (whole + sg.len - 1) / sg.len);
+    if (local >= segs || (Y ? sg.later != (local > 0) : local == 0 || local == segs - 1)) return;
+    const int t0 = begin + local * sg.len, len = min(sg.len, whole - local * sg.len);
     if (len <= 0 && (a.indices || !a.state_out)) return;
     long slot = seq;
     if (a.indices) {
@@ -132,16 +182,24 @@ template <int P, int S, typename ST> __global__ __launch_bounds__(256, 2) void s
     }
 
     // state: register 8u + 4k + b of tile nt is column n = 32 nt + 16 u + 8 hh + 4 k + b of row pcol
-    const int pcol = (l32 & 0x13) | ((l32 & 4) << 1) | ((l32 & 8) >> 1);
-    const long at = ((slot * a.heads + (active ? h : first)) * P + 32 * pc + pcol) * (long)S + 8 * hh;
+    const auto in_heads = [&](int l) {
+        const int pcol = (l & 0x13) | ((l & 4) << 1) | ((l & 8) >> 1);
+        return (long)((active ? h : first) * P + 32 * pc + pcol) * S + 8 * (l >> 5);
+    };
+    const long one = (long)a.heads * P * S;
     f32x16 st[C::NT];
+    const long in_head = in_heads(lane);
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
-            if (a.state_in) {
-                const ST *p = reinterpret_cast<const ST *>(a.state_in) + at + 32 * nt + 16 * u;
+            if (sg.later) {
+                const float *p = sg.states + (sl - 1) * one + in_head + 32 * nt + 16 * u;
+                x = load4(p);
+                y = load4(p + 4);
+            } else if (a.state_in && local == 0) {
+                const ST *p = reinterpret_cast<const ST *>(a.state_in) + slot * one + in_head + 32 * nt + 16 * u;
                 x = load4(p);
                 y = load4(p + 4);
             }
@@ -156,213 +214,330 @@ template <int P, int S, typename ST> __global__ __launch_bounds__(256, 2) void s
     const bf16 *xg = reinterpret_cast<const bf16 *>(a.x) + (long)t0 * a.x_stride + (long)first * P;
     const bf16 *bg = reinterpret_cast<const bf16 *>(a.B) + (long)t0 * a.b_stride + (long)g * S;
     const bf16 *cg = reinterpret_cast<const bf16 *>(a.C) + (long)t0 * a.c_stride + (long)g * S;
-    const unsigned xoff = (unsigned)((tid / 16) * a.x_stride + (tid % 16) * 8) * 2;
-    const unsigned boff = (unsigned)((tid / C::PPR) * a.b_stride + (tid % C::PPR) * 8) * 2;
-    const unsigned coff = (unsigned)((tid / C::PPR) * a.c_stride + (tid % C::PPR) * 8) * 2;
-    const bool xin = first + (tid % 16) * 8 / P < (g + 1) * rep;   // the piece's head is there
+    // z and y: row l32 of 32, the wave's columns
+    const bf16 *yg = uniform(reinterpret_cast<const bf16 *>(a.y) + (long)t0 * a.heads * P + (long)h * P + 32 * pc);
+    const bf16 *zg = uniform(reinterpret_cast<const bf16 *>(a.z) + (long)t0 * a.z_stride + (long)(active ? h : first) * P + 32 * pc);
     u32x4 xr[4], br[C::PB], cr[C::PB];
-    auto stage = [&](int c0) {   // rows past the sequence read as zero
-        const int rows = min(64, len - c0);
-        const __amdgpu_buffer_rsrc_t xs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<bf16 *>(xg + c0 * a.x_stride), 0, (int)(rows * a.x_stride * 2), kBufferWord3);
-        const __amdgpu_buffer_rsrc_t bs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<bf16 *>(bg + c0 * a.b_stride), 0, (int)(rows * a.b_stride * 2), kBufferWord3);
-        const __amdgpu_buffer_rsrc_t cs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<bf16 *>(cg + c0 * a.c_stride), 0, (int)(rows * a.c_stride * 2), kBufferWord3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            xr[i] = __builtin_amdgcn_raw_buffer_load_b128(xs, xin ? xoff + (unsigned)(16 * i * a.x_stride * 2) : 0x80000000u, 0, 0);
-#pragma unroll
-        for (int i = 0; i < C::PB; ++i) {
-            br[i] = __builtin_amdgcn_raw_buffer_load_b128(bs, boff + (unsigned)(256 / C::PPR * i * a.b_stride * 2), 0, 0);
-            cr[i] = __builtin_amdgcn_raw_buffer_load_b128(cs, coff + (unsigned)(256 / C::PPR * i * a.c_stride * 2), 0, 0);
-        }
+    // `each` rows from row `from`; rows past the sequence read as zero
+    auto rows_at = [&](const bf16 *base, long stride, int from, int each) {
+        // (clamped on the vector unit, whose result would make the load loop over descriptors)
+        const int rows = __builtin_amdgcn_readfirstlane(max(0, min(each, len - from)));
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16 *>(base + from * stride), 0, (int)(rows * stride * 2), kBufferWord3);
     };
-    auto unstage = [&]() {
+    // A burst of loads stalls the wave until the caches take them, so they are
+    // issued a few at a time: part q of 4 of x, of B, of C.
+    auto stage_x = [&](int c0, int lane, int q) {
+        const int tid = 64 * wave + lane;
+        const unsigned off = (unsigned)((tid / 16) * (int)a.x_stride + (tid % 16) * 8) * 2;
+        const bool in = first + (tid % 16) * 8 / P < (g + 1) * rep;   // the piece's head is there
+        xr[q] = __builtin_amdgcn_raw_buffer_load_b128(rows_at(xg, a.x_stride, c0 + 16 * q, 16), in ? off : 0x80000000u, 0, 0);
+    };
+    constexpr int each = 256 / C::PPR;   // rows of B and C a pass of the workgroup loads
+    auto stage_b = [&](int c0, int lane, int q) {
+        const int tid = 64 * wave + lane;
+        if (q < C::PB)
+            br[q] = __builtin_amdgcn_raw_buffer_load_b128(rows_at(bg, a.b_stride, c0 + each * q, each),
+                                                          (unsigned)((tid / C::PPR) * (int)a.b_stride + (tid % C::PPR) * 8) * 2, 0, 0);
+    };
+    auto stage_c = [&](int c0, int lane, int q) {
+        const int tid = 64 * wave + lane;
+        if (Y && q < C::PB)
+            cr[q] = __builtin_amdgcn_raw_buffer_load_b128(rows_at(cg, a.c_stride, c0 + each * q, each),
+                                                          (unsigned)((tid / C::PPR) * (int)a.c_stride + (tid % C::PPR) * 8) * 2, 0, 0);
+    };
+    auto unstage_xb = [&](int lane) {
+        const int tid = 64 * wave + lane;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<u32x4 *>(lds + (tid / 16 + 16 * i) * C::XROW + (tid % 16) * 16) = xr[i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4 *>(lds + tile_at<16>(tid / 16 + 16 * i, tid % 16)) = xr[i];
 #pragma unroll
-        for (int i = 0; i < C::PB; ++i) {
-            const int at_l = (tid / C::PPR + 256 / C::PPR * i) * C::BROW + (tid % C::PPR) * 16;
-            *reinterpret_cast<u32x4 *>(lds + C::OFF_B + at_l) = br[i];
-            *reinterpret_cast<u32x4 *>(lds + C::OFF_C + at_l) = cr[i];
-        }
+        for (int i = 0; i < C::PB; ++i)
+            *reinterpret_cast<u32x4 *>(lds + C::OFF_B + tile_at<C::PPR>(tid / C::PPR + each * i, tid % C::PPR)) = br[i];
+    };
+    auto unstage_c = [&](int lane) {
+        const int tid = 64 * wave + lane;
+#pragma unroll
+        for (int i = 0; i < C::PB; ++i)
+            *reinterpret_cast<u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(tid / C::PPR + each * i, tid % C::PPR)) = cr[i];
     };
 
     // gates, by the last wave of each head, a token a lane
     const bool gates = active && pc == C::WPH - 1;
-    const double A = gates ? -exp((double)a.A_log[h]) * 1.4426950408889634 : 0.0;
+    const double A = uniform(gates ? -exp((double)a.A_log[h]) * 1.4426950408889634 : 0.0);
     const float bias = gates && a.dt_bias ? a.dt_bias[h] : 0.f, Dh = active && a.D ? a.D[h] : 0.f;
     const bf16 *dg = reinterpret_cast<const bf16 *>(a.dt) + (long)t0 * a.dt_stride + h;
-    float dtv = 0.f;
-    auto fetch_dt = [&](int c0) {
-        dtv = 0.f;
-        if (gates && c0 + lane < len) dtv = io_traits<bf16>::load(dg, (long)(c0 + lane) * a.dt_stride);
+    uint32_t dtv = 0;       // bits, of a chunk ahead: converted when they are used
+    double through = 0.0;   // log2 of the segment's decay
+    auto fetch_dt = [&](int c0, int lane) {
+        dtv = reinterpret_cast<const uint16_t *>(dg)[(long)min(c0 + lane, len - 1) * a.dt_stride];
     };
-    auto make_gates = [&](int c0, int buf) {
-        if (!gates) return;
-        const float step = c0 + lane < len ? softplus_f(dtv + bias) : 0.f;
-        double G = (double)step * A;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const double o = __shfl_up(G, m, 64);
-            if (lane >= m) G += o;
-        }
-        const double last = __shfl(G, 63, 64);
+    auto make_gates = [&](int c0, int buf, int lane) {
+        const float step = c0 + lane < len ? softplus_f(lo_f(dtv) + bias) : 0.f;
+        const double G = wave_scan((double)step * A), last = lane_value(G, 63);
+        through = uniform(through + last);
         float *q = reinterpret_cast<float *>(lds + C::OFF_G + buf * C::GBYTES) + hs * kGateArrays * 64 + lane;
-        const float gh = (float)G;
+        const float gh = (float)G, gl = (float)(G - (double)gh);
         q[0] = gh;
-        q[64] = (float)(G - (double)gh);
-        q[128] = step;
+        q[64] = gl;
+        q[128] = step * __builtin_amdgcn_exp2f(-gl);
         q[192] = step * __builtin_amdgcn_exp2f((float)(last - G));
         q[256] = __builtin_amdgcn_exp2f(gh);
     };
 
     if (len > 0) {
-        stage(0);
-        fetch_dt(0);
-        make_gates(0, 0);
+        if (gates) {
+            fetch_dt(0, lane);
+            make_gates(0, 0, lane);
+            fetch_dt(64, lane);   // a chunk ahead of its use: memory answers in order, and the rows' loads are slower
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            stage_x(0, lane, q);
+            stage_b(0, lane, q);
+            stage_c(0, lane, q);
+        }
+        if constexpr (Y && C::WPH > 1) unstage_c(lane);
     }
-    // transposed reads: row (of 4) and column piece of this lane within a 32-column block
-    const int trow = 4 * hh + ((lane & 15) >> 2);
-    const int tcol = 32 * ((lane >> 4) & 1) + 8 * (((lane & 1) << 1) | ((lane >> 1) & 1));   // bytes
-    unsigned char *const mbase = lds + C::OFF_M + hs * C::MBYTES + lane * 16;
-
     int buf = 0;
+    const int lane0 = lane;
     for (int c0 = 0; c0 < len; c0 += 64, buf ^= 1) {
-        unstage();
+        // What depends on the lane is formed anew in every chunk: kept through
+        // the loop it takes some 40 registers, and what is spilled for them
+        // waits, when it is read back, for the rows on their way.
+        int lane = lane0;
+        asm volatile("" : "+v"(lane));
+        lane &= 63;
+        const int hh = lane >> 5, l32 = lane & 31;
+        // transposed reads: row (of 4) and column piece (8 bytes) of this lane within a 32-column block
+        const int trow = 4 * hh + ((lane & 15) >> 2), tpiece = 2 * ((lane >> 4) & 1) + (lane & 1), thalf = (lane & 2) << 2;
+        unsigned char *const mbase = lds + C::OFF_M + hs * C::MBYTES + lane * 16;
+        unstage_xb(lane);
+        if constexpr (Y && C::WPH == 1) unstage_c(lane);
         __syncthreads();
         const float *gate = reinterpret_cast<const float *>(lds + C::OFF_G + buf * C::GBYTES) + hs * kGateArrays * 64;
-        // z of this chunk (used last) and the next chunk's rows: in flight meanwhile
-        u32x4 zr[2][2];
-        if (a.z) {
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                const int t = c0 + 32 * tt + l32;
-                const bf16 *zp = reinterpret_cast<const bf16 *>(a.z) + (long)(t0 + min(t, len - 1)) * a.z_stride +
-                                 (long)(active ? h : first) * P + 32 * pc + 8 * hh;
-                zr[tt][0] = *reinterpret_cast<const u32x4 *>(zp);
-                zr[tt][1] = *reinterpret_cast<const u32x4 *>(zp + 16);
-            }
-        }
         const bool more = c0 + 64 < len;
-        if (more) {
-            stage(c0 + 64);
-            fetch_dt(c0 + 64);
-        }
+        // The next chunk's C is loaded here and takes this one's place after the
+        // barrier below; x and B are loaded after that one, for the loop's head.
+        // (Past the end there are no rows and the loads return zeros: no branch.)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) stage_c(c0 + 64, lane, q);
 
-        // C_t . B_s, and M from it: tiles (t, s) = (0, 0), (1, 0), (1, 1) shared by the head's waves
-        u32x4 m[C::WPH == 1 ? 3 : 1][2][2];
-        if (active) {
+        // C_t . B_s: tiles (t, s) = (0, 0), (1, 0), (1, 1), shared by the waves of
+        // a head; a head's only wave forms them where it uses them
+        auto products = [&](int tt, int ss) {
+            f32x16 acc;
 #pragma unroll
-            for (int tile = 0; tile < 3; ++tile) {
-                const int owner = C::WPH == 4 ? tile : C::WPH == 2 ? tile & 1 : 0;
-                if (owner != pc) continue;
-                const int tt = tile > 0, ss = tile > 1;
-                f32x16 acc;
+            for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll
-                for (int u = 0; u < S / 16; ++u) {
-                    const u32x4 bo = *reinterpret_cast<const u32x4 *>(lds + C::OFF_B + (32 * ss + l32) * C::BROW + 32 * u + 16 * hh);
-                    const u32x4 co = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + (32 * tt + l32) * C::BROW + 32 * u + 16 * hh);
-                    acc = mfma(bo, co, acc);
-                }
-                constexpr bool own = C::WPH == 1;
-                u32x4(&mt)[2][2] = m[own ? tile : 0];
-                m_tile(acc, gate, tt, ss, lane, Dh, mt);
-                if constexpr (!own) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) *reinterpret_cast<u32x4 *>(mbase + (tile * 4 + u * 2 + k) * 1024) = mt[u][k];
-                }
+            for (int u = 0; u < S / 16; ++u) {
+                const u32x4 bo = *reinterpret_cast<const u32x4 *>(lds + C::OFF_B + tile_at<C::PPR>(32 * ss + l32, 2 * u + hh));
+                const u32x4 co = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(32 * tt + l32, 2 * u + hh));
+                acc = mfma(bo, co, acc);
             }
-            if (more) make_gates(c0 + 64, buf ^ 1);
-        }
-
-        // y = exp(G) S C
-        f32x16 y[2];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[0][i] = y[1][i] = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt)
+            return acc;
+        };
+        auto form_m = [&](int tt, int ss, u32x4(&mt)[2][2]) {
+            const f32x16 cb = products(tt, ss);
+            const float gt = gate[32 * tt + l32], lt = gate[64 + 32 * tt + l32];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
+                float v[2][4], all[8];
+                m_part(cb, gate, tt, ss, 2 * u, lane, Dh, gt, lt, v[0]);
+                m_part(cb, gate, tt, ss, 2 * u + 1, lane, Dh, gt, lt, v[1]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) all[e] = v[e / 4][e % 4];
+                split<2>(all, mt[u]);
+            }
+        };
+        u32x4 m[2][2][2];
+        if (gates && more) {
+            make_gates(c0 + 64, buf ^ 1, lane);
+            fetch_dt(c0 + 128, lane);
+        }
+
+        // y = exp(G) S C, and under these products the arithmetic of M's tiles
+        // tile0 .. tile0 + TILES - 1
+        f32x16 y[2];
+        auto from_state = [&](auto count, int tile0) {
+            constexpr int TILES = decltype(count)::value, NS = S / 16;
+            f32x16 cb[TILES > 0 ? TILES : 1];
+            float gt[TILES > 0 ? TILES : 1], lt[TILES > 0 ? TILES : 1], mv[8];
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) {
+                const int tt = tile0 + j > 0;
+                cb[j] = products(tt, tile0 + j > 1);
+                gt[j] = gate[32 * tt + l32];
+                lt[j] = gate[64 + 32 * tt + l32];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[0][i] = y[1][i] = 0.f;
+            u32x4 co[2];   // C's operand of one step ahead
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+                co[tt] = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(32 * tt + l32, hh));
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                u32x4 cn[2];
+                if (i + 1 < NS) {
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+                        cn[tt] = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(32 * tt + l32, 2 * (i + 1) + hh));
+                }
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = st[nt][8 * u + e];
+                for (int e = 0; e < 8; ++e) v[e] = st[i / 2][8 * (i % 2) + e];
                 u32x4 s[2];
                 split<2>(v, s);
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    const u32x4 co = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + (32 * tt + l32) * C::BROW + 64 * nt + 32 * u + 16 * hh);
-                    y[tt] = mfma(s[0], co, y[tt]);
-                    y[tt] = mfma(s[1], co, y[tt]);
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(s[j], co[tt], y[tt]);
+#pragma unroll
+                for (int part = i * 4 * TILES / NS; part < (i + 1) * 4 * TILES / NS; ++part) {
+                    const int j = part / 4, q = part % 4, tile = tile0 + j;
+                    float v4[4];
+                    m_part(cb[j], gate, tile > 0, tile > 1, q, lane, Dh, gt[j], lt[j], v4);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) mv[4 * (q % 2) + b] = v4[b];
+                    if (q % 2) {
+                        u32x4 mt[2];
+                        split<2>(mv, mt);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) *reinterpret_cast<u32x4 *>(mbase + (tile * 4 + q / 2 * 2 + k) * 1024) = mt[k];
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {   // a product, then arithmetic that runs under it
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, TILES == 0 ? 7 : 11, 0);
+                }
+                co[0] = cn[0];
+                co[1] = cn[1];
             }
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-            const float e = gate[256 + 32 * tt + l32];
+            for (int tt = 0; tt < 2; ++tt) {
+                const float e = gate[256 + 32 * tt + l32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[tt][i] *= e;
+                for (int i = 0; i < 16; ++i) y[tt][i] *= e;
+            }
+        };
+        if constexpr (Y) {
+            using std::integral_constant;
+            // tiles of M by wave: 0, 1, 2 and none, or 0, 1 and 2 (the last wave has the gates)
+            if (C::WPH == 4 && active && pc < 3) from_state(integral_constant<int, 1>{}, pc);
+            else if (C::WPH == 2 && active && pc == 0) from_state(integral_constant<int, 2>{}, 0);
+            else if (C::WPH == 2 && active) from_state(integral_constant<int, 1>{}, 2);
+            else from_state(integral_constant<int, 0>{}, 0);
         }
         const float all = gate[256 + 63];
-#pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) st[nt][i] *= all;
-        if constexpr (C::WPH > 1) __syncthreads();
+        if constexpr (Y && C::WPH > 1) __syncthreads();   // M is there; C is no longer needed
+        __builtin_amdgcn_sched_barrier(0);
 
-        // y += M x;  S += (weights x) B^T, 16 tokens at a time
+        // y += M x;  S += (weights x) B^T, 16 tokens at a time, B's operands two
+        // products ahead, with the next chunk's rows loaded in between
+        u32x4 zr[2][2], xo, bo[3], mo[2][2];
+        f32x4 w[2];
+        auto operand_x = [&](int k) {
+            const u32x2 x0 = lds_tr(lds + tile_at<16>(16 * k + trow, 4 * wave + tpiece) + thalf);
+            const u32x2 x1 = lds_tr(lds + tile_at<16>(16 * k + trow + 8, 4 * wave + tpiece) + thalf);
+            return u32x4{x0[0], x0[1], x1[0], x1[1]};
+        };
+        auto operand_b = [&](int step) {
+            const int row = 16 * (step / C::NT) + trow, piece = 4 * (step % C::NT) + tpiece;
+            const u32x2 b0 = lds_tr(lds + C::OFF_B + tile_at<C::PPR>(row, piece) + thalf);
+            const u32x2 b1 = lds_tr(lds + C::OFF_B + tile_at<C::PPR>(row + 8, piece) + thalf);
+            return u32x4{b0[0], b0[1], b1[0], b1[1]};
+        };
+        auto operands_m = [&](int k) {
+            if constexpr (Y && C::WPH > 1) {
+#pragma unroll
+                for (int tt = k >> 1; tt < 2; ++tt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        mo[tt][j] = *reinterpret_cast<const u32x4 *>(mbase + ((tt + (k >> 1)) * 4 + (k & 1) * 2 + j) * 1024);
+            }
+        };
+        auto weights = [&](int k) {
+            w[0] = *reinterpret_cast<const f32x4 *>(gate + 192 + 16 * k + 4 * hh);
+            w[1] = *reinterpret_cast<const f32x4 *>(gate + 192 + 16 * k + 8 + 4 * hh);
+        };
+        // words e of the three terms of weight x x
+        u32x4 wx[3];
+        auto weigh = [&](int e) {
+            float p = lo_f(xo[e]) * w[e / 2][2 * e % 4], q = hi_f(xo[e]) * w[e / 2][(2 * e + 1) % 4];
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const uint32_t t = pack2(p, q);
+                wx[j][e] = t;
+                p -= lo_f(t);
+                q -= hi_f(t);
+            }
+        };
+        xo = operand_x(0);
+        operands_m(0);
+        weights(0);
+        bo[0] = operand_b(0);
+        bo[1] = operand_b(1);
+        // (a head's only wave still forms M from C below: its workgroup waits for the loop's head)
+        if constexpr (Y && C::WPH > 1) unstage_c(lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) weigh(e);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int ss = k >> 1, u = k & 1;
-            const int row = 16 * k + trow;
-            const unsigned char *xp = lds + row * C::XROW + 64 * wave + tcol;
-            const u32x2 x0 = lds_tr(xp), x1 = lds_tr(xp + 8 * C::XROW);
-            const u32x4 xo = {x0[0], x0[1], x1[0], x1[1]};
+            stage_x(c0 + 64, lane, k);
+            stage_b(c0 + 64, lane, k);
+            if (Y && k == 2 && a.z) {   // z of this chunk
+                const unsigned zoff = (unsigned)(l32 * (int)a.z_stride + 8 * hh) * 2;
 #pragma unroll
-            for (int tt = ss; tt < 2; ++tt) {
-                const int tile = tt + ss;
-                u32x4 m0, m1;
-                if constexpr (C::WPH == 1) {
-                    m0 = m[tile][u][0];
-                    m1 = m[tile][u][1];
-                } else {
-                    m0 = *reinterpret_cast<const u32x4 *>(mbase + (tile * 4 + u * 2) * 1024);
-                    m1 = *reinterpret_cast<const u32x4 *>(mbase + (tile * 4 + u * 2 + 1) * 1024);
+                for (int tt = 0; tt < 2; ++tt) {
+                    const __amdgpu_buffer_rsrc_t zs = rows_at(zg, a.z_stride, c0 + 32 * tt, 32);
+                    zr[tt][0] = __builtin_amdgcn_raw_buffer_load_b128(zs, zoff, 0, 0);
+                    zr[tt][1] = __builtin_amdgcn_raw_buffer_load_b128(zs, zoff + 32, 0, 0);
                 }
-                y[tt] = mfma(xo, m0, y[tt]);
-                y[tt] = mfma(xo, m1, y[tt]);
             }
-            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(gate + 192 + 16 * k + 4 * hh);
-            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(gate + 192 + 16 * k + 8 + 4 * hh);
-            float v[8];
+            if constexpr (Y && C::WPH == 1) {
+                if (u == 0) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                v[2 * e] = lo_f(xo[e]) * w0[2 * e];
-                v[2 * e + 1] = hi_f(xo[e]) * w0[2 * e + 1];
-                v[4 + 2 * e] = lo_f(xo[2 + e]) * w1[2 * e];
-                v[5 + 2 * e] = hi_f(xo[2 + e]) * w1[2 * e + 1];
+                    for (int tt = ss; tt < 2; ++tt) form_m(tt, ss, m[tt]);
+                }
             }
-            u32x4 wx[3];
-            split<3>(v, wx);
+            if constexpr (Y) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int tt = ss; tt < 2; ++tt) y[tt] = mfma(xo, C::WPH == 1 ? m[tt][u][j] : mo[tt][j], y[tt]);
+            }
+            // The next 16 tokens' weighted x is split between this one's products,
+            // and the state decays just before its first.
+            const u32x4 w0 = wx[0], w1 = wx[1], w2 = wx[2];
 #pragma unroll
             for (int nt = 0; nt < C::NT; ++nt) {
-                const unsigned char *bp = lds + C::OFF_B + row * C::BROW + 64 * nt + tcol;
-                const u32x2 b0 = lds_tr(bp), b1 = lds_tr(bp + 8 * C::BROW);
-                const u32x4 bo = {b0[0], b0[1], b1[0], b1[1]};
+                const int step = k * C::NT + nt;
+                if (step + 2 < 4 * C::NT) bo[(step + 2) % 3] = operand_b(step + 2);
+                if (nt == 0 && k < 3) {
+                    xo = operand_x(k + 1);
+                    weights(k + 1);
+                    operands_m(k + 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);   // each product keeps the arithmetic that runs under it
+                if (k == 0) {
 #pragma unroll
-                for (int j = 0; j < 3; ++j) st[nt] = mfma(bo, wx[j], st[nt]);
+                    for (int i = 0; i < 16; ++i) st[nt][i] *= all;
+                }
+                st[nt] = mfma(bo[step % 3], w0, st[nt]);
+                st[nt] = mfma(bo[step % 3], w1, st[nt]);
+                st[nt] = mfma(bo[step % 3], w2, st[nt]);
+                if (k < 3) {
+#pragma unroll
+                    for (int e = nt * 4 / C::NT; e < (nt + 1) * 4 / C::NT; ++e) weigh(e);
+                }
             }
         }
 
-        if (active) {
+        if (Y && active) {
+            const unsigned yoff = (unsigned)(l32 * a.heads * P + 8 * hh) * 2;
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-                const int t = c0 + 32 * tt + l32;
                 if (a.z) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
@@ -373,71 +548,143 @@ template <int P, int S, typename ST> __global__ __launch_bounds__(256, 2) void s
                             y[tt][8 * u + 2 * i + 1] *= z1 * sigmoid_f(z1);
                         }
                 }
-                if (t < len) {
-                    bf16 *yp = reinterpret_cast<bf16 *>(a.y) + ((long)(t0 + t) * a.heads + h) * P + 32 * pc + 8 * hh;
+                const __amdgpu_buffer_rsrc_t ys = rows_at(yg, (long)a.heads * P, c0 + 32 * tt, 32);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        u32x4 w;
+                for (int u = 0; u < 2; ++u) {
+                    u32x4 w;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(y[tt][8 * u + 2 * i], y[tt][8 * u + 2 * i + 1]);
-                        *reinterpret_cast<u32x4 *>(yp + 16 * u) = w;
-                    }
+                    for (int i = 0; i < 4; ++i) w[i] = pack2(y[tt][8 * u + 2 * i], y[tt][8 * u + 2 * i + 1]);
+                    __builtin_amdgcn_raw_buffer_store_b128(w, ys, yoff + 32 * u, 0, 0);
                 }
             }
         }
         __syncthreads();   // every wave has read this chunk
     }
 
-    if (a.state_out && active) {
+    const bool last = local == segs - 1;   // else the state goes to the segment's place
+    if (!active || (last ? !a.state_out : sg.later)) return;
+    if (!last && gates && lane == 0) sg.decays[(long)sl * a.heads + h] = __builtin_amdgcn_exp2f((float)through);
+    int again = lane;   // the offsets formed anew, not kept through the loop
+    asm volatile("" : "+v"(again));
+    const long out_head = in_heads(again);
 #pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt)
+    for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                ST *p = reinterpret_cast<ST *>(a.state_out) + at + 32 * nt + 16 * u;
-                if constexpr (sizeof(ST) == 4) {
+        for (int u = 0; u < 2; ++u) {
+            f32x4 x[2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const f32x4 x = {st[nt][8 * u + 4 * k], st[nt][8 * u + 4 * k + 1], st[nt][8 * u + 4 * k + 2],
-                                         st[nt][8 * u + 4 * k + 3]};
-                        *reinterpret_cast<f32x4 *>(p + 4 * k) = x;
-                    }
-                } else {
-                    u32x4 w;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(st[nt][8 * u + 2 * i], st[nt][8 * u + 2 * i + 1]);
-                    *reinterpret_cast<u32x4 *>(p) = w;
-                }
+            for (int e = 0; e < 8; ++e) x[e / 4][e % 4] = st[nt][8 * u + e];
+            if (!last) {
+                float *p = sg.states + sl * one + out_head + 32 * nt + 16 * u;
+                *reinterpret_cast<f32x4 *>(p) = x[0];
+                *reinterpret_cast<f32x4 *>(p + 4) = x[1];
+                continue;
             }
+            ST *p = reinterpret_cast<ST *>(a.state_out) + slot * one + out_head + 32 * nt + 16 * u;
+            if constexpr (sizeof(ST) == 4) {
+                *reinterpret_cast<f32x4 *>(p) = x[0];
+                *reinterpret_cast<f32x4 *>(p + 4) = x[1];
+            } else {
+                const u32x4 w = {pack2(x[0][0], x[0][1]), pack2(x[0][2], x[0][3]), pack2(x[1][0], x[1][1]), pack2(x[1][2], x[1][3])};
+                *reinterpret_cast<u32x4 *>(p) = w;
+            }
+        }
+}
+
+// states[k] = decays[k] states[k - 1] + states[k] over a sequence's segments
+// between its first and its last.  grid (quads of a state, sequences on y and z)
+__global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Segments sg) {
+    const int seq = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
+    if (seq >= a.num_seqs) return;
+    const long one = (long)a.heads * a.p * a.s, at = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int begin = a.cu_seqlens[seq], segs = (a.cu_seqlens[seq + 1] - begin + sg.len - 1) / sg.len;
+    if (segs < 3 || at >= one) return;
+    const long sl = begin / sg.len + seq;
+    const float *dec = sg.decays + sl * a.heads + at / (a.p * a.s);
+    float *p = sg.states + sl * one + at;
+    f32x4 s = load4(p);
+    for (int k = 1; k < segs - 1; ++k) {
+        const f32x4 x = load4(p + k * one);
+        s = dec[(long)k * a.heads] * s + x;
+        *reinterpret_cast<f32x4 *>(p + k * one) = s;
     }
 }
 
-template <int P, int S, typename ST> static hipError_t launch_chunk(const SsmArgs &a, hipStream_t stream) {
+// Tokens of a segment: as many as leave the chip's 512 resident workgroups
+// about two segments each, at least four chunks.
+static int segment_tokens(int num_seqs, int total_tokens, int wgs) {
+    const long len = ((long)total_tokens * wgs / 1024 + 63) / 64 * 64;
+    return (int)(len < 256 ? 256 : len);
+}
+static int head_workgroups(int heads, int groups, int p) {
+    const int hw = 128 / p, rep = heads / groups;
+    return groups * ((rep + hw - 1) / hw);
+}
+static Segments segments_of(int num_seqs, int total_tokens, int heads, int groups, int p) {
+    Segments sg{};
+    sg.len = segment_tokens(num_seqs, total_tokens, head_workgroups(heads, groups, p));
+    if (sg.len >= total_tokens) {   // every sequence is one segment
+        sg.len = (total_tokens + 64) / 64 * 64;
+        sg.slots = num_seqs;
+    } else {
+        sg.slots = total_tokens / sg.len + num_seqs;
+    }
+    return sg;
+}
+
+size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int groups, int p, int s, bool io_bf16) {
+    if (!io_bf16 || num_seqs <= 0) return 0;
+    const Segments sg = segments_of(num_seqs, total_tokens, heads, groups, p);
+    if (sg.slots == num_seqs) return 0;
+    return (size_t)sg.slots * heads * ((size_t)p * s + 1) * sizeof(float);
+}
+
+template <int P, int S, typename ST> static hipError_t launch_chunk(const SsmArgs &a, void *workspace, hipStream_t stream) {
     using C = Chunk<P, S>;
     static_assert(C::LDS <= 163840, "LDS");
-    const int rep = a.heads / a.groups;
-    const dim3 grid(a.num_seqs * a.groups * ((rep + C::HW - 1) / C::HW));
-    ssm_chunk_kernel<P, S, ST><<<grid, 256, C::LDS, stream>>>(a);
+    Segments sg = segments_of(a.num_seqs, a.total_tokens, a.heads, a.groups, a.p);
+    const dim3 grid(sg.slots * head_workgroups(a.heads, a.groups, P));
+    const auto whole = ssm_chunk_kernel<P, S, ST, true>, alone = ssm_chunk_kernel<P, S, ST, false>;
+    hipError_t e;
+    if ((e = hipFuncSetAttribute((const void *)whole, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS)) != hipSuccess) return e;
+    if (sg.slots == a.num_seqs) {
+        whole<<<grid, 256, C::LDS, stream>>>(a, sg);
+        return hipGetLastError();
+    }
+    const size_t one = (size_t)a.heads * P * S;
+    sg.states = static_cast<float *>(workspace);
+    sg.decays = sg.states + sg.slots * one;
+    whole<<<grid, 256, C::LDS, stream>>>(a, sg);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (2L * sg.len < a.total_tokens) {   // a sequence of three segments may be there
+        if ((e = hipFuncSetAttribute((const void *)alone, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS)) != hipSuccess) return e;
+        alone<<<grid, 256, C::LDS, stream>>>(a, sg);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        ssm_carry_kernel<<<dim3((unsigned)((one / 4 + 255) / 256), decode_grid_y(a.num_seqs), decode_grid_z(a.num_seqs)), 256, 0,
+                           stream>>>(a, sg);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    sg.later = true;
+    whole<<<grid, 256, C::LDS, stream>>>(a, sg);
     return hipGetLastError();
 }
-template <int P, int S> static hipError_t launch_st(const SsmArgs &a, hipStream_t s) {
-    return a.state_bf16 ? launch_chunk<P, S, bf16>(a, s) : launch_chunk<P, S, float>(a, s);
+template <int P, int S> static hipError_t launch_st(const SsmArgs &a, void *w, hipStream_t s) {
+    return a.state_bf16 ? launch_chunk<P, S, bf16>(a, w, s) : launch_chunk<P, S, float>(a, w, s);
 }
-template <int P> static hipError_t launch_s(const SsmArgs &a, hipStream_t s) {
+template <int P> static hipError_t launch_s(const SsmArgs &a, void *w, hipStream_t s) {
     switch (a.s) {
-    case 32: return launch_st<P, 32>(a, s);
-    case 64: return launch_st<P, 64>(a, s);
-    default: return launch_st<P, 128>(a, s);
+    case 32: return launch_st<P, 32>(a, w, s);
+    case 64: return launch_st<P, 64>(a, w, s);
+    default: return launch_st<P, 128>(a, w, s);
     }
 }
 
-size_t ssm_prefill_workspace_bytes(int, int, int, int, int, bool) { return 0; }
-
-hipError_t launch_ssm_prefill(const SsmArgs &a, void *, hipStream_t s) {
+hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t s) {
     if (!a.io_bf16) return launch_ssm_run(a, s);
     switch (a.p) {
-    case 32: return launch_s<32>(a, s);
-    case 64: return launch_s<64>(a, s);
-    default: return launch_s<128>(a, s);
+    case 32: return launch_s<32>(a, workspace, s);
+    case 64: return launch_s<64>(a, workspace, s);
+    default: return launch_s<128>(a, workspace, s);
     }
 }
 
