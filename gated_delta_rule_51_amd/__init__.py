@@ -555,22 +555,59 @@ def recurrent_decode_packed_fused_gate(qkv, gate_x, A_log, dt_bias, beta_x, stat
 # ---- short causal convolution, state-space scan, drafts ---------------------
 
 
+# A one-token step takes a few microseconds on the GPU, so what runs around it
+# on the host counts: the checks below test everything in one expression and
+# only then, where it does not hold, find out what to say.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, current stream of dev) with dev the current device."""
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, _raw_stream(dev.index) if _raw_stream else _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)))
+
+
 def _token_rows(t, name, dtype, n, tail):
-    """t must be [>= n, *tail], contiguous within a row; rows may lie apart (a
-    slice of a wider row).  Returns the elements between two rows."""
+    """t must be [>= n, *tail] (one or two sizes), contiguous within a row; rows
+    may lie apart (a slice of a wider row).  Returns the elements between two
+    rows."""
+    shape, stride = t.shape, t.stride()
+    if len(tail) == 2:
+        a, b = tail
+        width = a * b
+        ok = len(shape) == 3 and shape[1] == a and shape[2] == b and (stride[2] == 1 or b == 1) and (stride[1] == b or a == 1)
+    else:
+        width = tail[0]
+        ok = len(shape) == 2 and shape[1] == width and (stride[1] == 1 or width == 1)
+    if ok and t.dtype is dtype and shape[0] >= n:
+        if shape[0] <= 1:
+            return width
+        if stride[0] >= width:
+            return stride[0]
+        raise ValueError("%s must have rows that do not overlap" % name)
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     _rows(t, name, n, tail)
-    width = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != width:
-            raise ValueError("%s must be contiguous within a row" % name)
-        width *= size
-    if t.shape[0] <= 1:
-        return width
-    if t.stride(0) < width:
-        raise ValueError("%s must have rows that do not overlap" % name)
-    return t.stride(0)
+    raise ValueError("%s must be contiguous within a row" % name)
+
+
+def _whole(t, name, dtype, n, tail):
+    """t, if given, must be contiguous [>= n, *tail]."""
+    if t is None or (t.dtype is dtype and t.shape[1:] == tail and t.dim() == 1 + len(tail) and t.shape[0] >= n and t.is_contiguous()):
+        return
+    _need(t, name, dtype, 1 + len(tail))
+    _rows(t, name, n, tail)
+
+
+def _per_head(t, name, n):
+    if t is None or (t.dtype is torch.float32 and t.shape == (n,) and t.is_contiguous()):
+        return
+    _need(t, name, torch.float32, 1)
+    raise ValueError("%s must have shape [%d], got %s" % (name, n, tuple(t.shape)))
 
 
 def _scratch(nbytes, device):
@@ -580,8 +617,8 @@ def _scratch(nbytes, device):
 
 
 def _cu(cu_seqlens):
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    n = cu_seqlens.numel() - 1
+    _whole(cu_seqlens, "cu_seqlens", torch.int32, 0, ())
+    n = cu_seqlens.shape[0] - 1
     if n < 0:
         raise ValueError("cu_seqlens must hold N + 1 >= 1 offsets")
     return n
@@ -592,11 +629,11 @@ def _conv_args(x, weight, bias):
         raise ValueError("x must be [T, D]")
     dt = _io_dtype(x)
     T, D = x.shape
-    _need(weight, "weight", x.dtype, 2)
-    if weight.shape[0] != D:
+    if not (weight.dtype is x.dtype and weight.dim() == 2 and weight.shape[0] == D and weight.is_contiguous()):
+        _need(weight, "weight", x.dtype, 2)
         raise ValueError("weight must have shape [%d, W], got %s" % (D, tuple(weight.shape)))
-    _need(bias, "bias", x.dtype, 1)
-    if bias is not None and bias.shape[0] != D:
+    if bias is not None and not (bias.dtype is x.dtype and bias.shape == (D,) and bias.is_contiguous()):
+        _need(bias, "bias", x.dtype, 1)
         raise ValueError("bias must have shape [%d], got %s" % (D, tuple(bias.shape)))
     return dt, T, D, weight.shape[1], _token_rows(x, "x", x.dtype, T, (D,))
 
@@ -617,20 +654,17 @@ def conv_prefill(x, weight, bias, cu_seqlens, *, initial_state=None, state_indic
     if activation not in ("silu", None):
         raise ValueError("activation must be 'silu' or None")
     N = _cu(cu_seqlens)
-    _need(initial_state, "initial_state", x.dtype, 3)
-    _need(state_indices, "state_indices", torch.int32, 1)
     pool = state_indices is not None
     if pool and initial_state is None:
         raise ValueError("pool mode needs the pool as initial_state")
-    _rows(initial_state, "state pool" if pool else "initial_state", 1 if pool else N, (W - 1, D))
-    _rows(state_indices, "state_indices", N, ())
+    _whole(initial_state, "state pool" if pool else "initial_state", x.dtype, 1 if pool else N, (W - 1, D))
+    _whole(state_indices, "state_indices", torch.int32, N, ())
     dev = _on_device(x, (weight, bias, cu_seqlens, initial_state, state_indices))
     desc = ConvDesc(N, T, D, W, dt, 1 if activation else 0, initial_state.shape[0] if pool else 0, 1 if update_pool else 0, stride)
     y = torch.empty(T, D, dtype=x.dtype, device=dev)
     final = initial_state if pool else (torch.empty(N, W - 1, D, dtype=x.dtype, device=dev) if output_final_state else None)
-    with torch.cuda.device(dev):
-        _check(lib().kda_conv_prefill(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(initial_state),
-                                      _ptr(state_indices), None if pool else _ptr(final), _ptr(y), _stream(dev)))
+    _launch(dev, lib().kda_conv_prefill, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(initial_state),
+            _ptr(state_indices), None if pool else _ptr(final), _ptr(y))
     return y, final
 
 
@@ -640,16 +674,13 @@ def conv_decode(x, weight, bias, conv_pool, state_indices, *, activation="silu")
     dt, B, D, W, stride = _conv_args(x, weight, bias)
     if activation not in ("silu", None):
         raise ValueError("activation must be 'silu' or None")
-    _need(conv_pool, "conv_pool", x.dtype, 3)
-    _need(state_indices, "state_indices", torch.int32, 1)
-    _rows(conv_pool, "conv_pool", 1, (W - 1, D))
-    _rows(state_indices, "state_indices", B, ())
+    _whole(conv_pool, "conv_pool", x.dtype, 1, (W - 1, D))
+    _whole(state_indices, "state_indices", torch.int32, B, ())
     dev = _on_device(x, (weight, bias, conv_pool, state_indices))
     desc = ConvDesc(B, B, D, W, dt, 1 if activation else 0, conv_pool.shape[0], 1, stride)
     y = torch.empty(B, D, dtype=x.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().kda_conv_decode(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_pool), _ptr(state_indices),
-                                     _ptr(y), _stream(dev)))
+    _launch(dev, lib().kda_conv_decode, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_pool), _ptr(state_indices),
+            _ptr(y))
     return y
 
 
@@ -662,17 +693,15 @@ def conv_commit(x, cu_seqlens, steps, conv_pool, state_indices):
     T, D = x.shape
     stride = _token_rows(x, "x", x.dtype, T, (D,))
     N = _cu(cu_seqlens)
-    _need(conv_pool, "conv_pool", x.dtype, 3)
-    _need(state_indices, "state_indices", torch.int32, 1)
-    _need(steps, "steps", torch.int32, 1)
-    _rows(conv_pool, "conv_pool", 1, (conv_pool.shape[1], D))
-    _rows(state_indices, "state_indices", N, ())
-    _rows(steps, "steps", N, ())
+    if conv_pool.dim() != 3:
+        raise ValueError("conv_pool must be [slots, W - 1, D]")
+    _whole(conv_pool, "conv_pool", x.dtype, 1, (conv_pool.shape[1], D))
+    _whole(state_indices, "state_indices", torch.int32, N, ())
+    _whole(steps, "steps", torch.int32, N, ())
     dev = _on_device(x, (cu_seqlens, steps, conv_pool, state_indices))
     desc = ConvDesc(N, T, D, conv_pool.shape[1] + 1, _io_dtype(x), 0, conv_pool.shape[0], 1, stride)
-    with torch.cuda.device(dev):
-        _check(lib().kda_conv_commit(ctypes.byref(desc), _ptr(x), _ptr(cu_seqlens), _ptr(steps), _ptr(conv_pool),
-                                     _ptr(state_indices), _stream(dev)))
+    _launch(dev, lib().kda_conv_commit, ctypes.byref(desc), _ptr(x), _ptr(cu_seqlens), _ptr(steps), _ptr(conv_pool),
+            _ptr(state_indices))
 
 
 def _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, num_seqs, state_dtype):
@@ -687,16 +716,14 @@ def _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, num_seqs, state_dtype):
         raise ValueError("heads (%d) must be a multiple of groups (%d)" % (H, G))
     if state_dtype not in _DT:
         raise ValueError("states must be float32 or bfloat16")
-    desc = SsmDesc(num_seqs, T, H, G, P, S, _io_dtype(x), _DT[state_dtype], 0, 0, 0, 0)
-    desc.x_stride = _token_rows(x, "x", x.dtype, T, (H, P))
-    desc.dt_stride = _token_rows(dt, "dt", x.dtype, T, (H,))
-    desc.b_stride = _token_rows(B, "B", x.dtype, T, (G, S))
-    desc.c_stride = _token_rows(C, "C", x.dtype, T, (G, S))
-    desc.z_stride = 0 if z is None else _token_rows(z, "z", x.dtype, T, (H, P))
-    for t, name in ((A_log, "A_log"), (D, "D"), (dt_bias, "dt_bias")):
-        _need(t, name, torch.float32, 1)
-        if t is not None and t.shape[0] != H:
-            raise ValueError("%s must have shape [%d], got %s" % (name, H, tuple(t.shape)))
+    dtype = x.dtype
+    desc = SsmDesc(num_seqs, T, H, G, P, S, _io_dtype(x), _DT[state_dtype], 0, 0, 0, 0,
+                   _token_rows(x, "x", dtype, T, (H, P)), _token_rows(dt, "dt", dtype, T, (H,)),
+                   _token_rows(B, "B", dtype, T, (G, S)), _token_rows(C, "C", dtype, T, (G, S)),
+                   0 if z is None else _token_rows(z, "z", dtype, T, (H, P)))
+    _per_head(A_log, "A_log", H)
+    _per_head(D, "D", H)
+    _per_head(dt_bias, "dt_bias", H)
     return desc
 
 
@@ -709,43 +736,38 @@ def ssm_prefill(x, dt, A_log, B, C, cu_seqlens, *, D=None, z=None, dt_bias=None,
     Returns (y, final_state); dense and pool mode as for chunk_prefill, a state
     being [H, P, S]."""
     N = _cu(cu_seqlens)
-    _need(initial_state, "initial_state", None, 4)
-    _need(state_indices, "state_indices", torch.int32, 1)
     pool = state_indices is not None
     if pool and initial_state is None:
         raise ValueError("pool mode needs the pool as initial_state")
     sd = initial_state.dtype if initial_state is not None else (state_dtype or torch.float32)
     desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, N, sd)
     one = (desc.heads, desc.head_dim, desc.state_dim)
-    _rows(initial_state, "state pool" if pool else "initial_state", 1 if pool else N, one)
-    _rows(state_indices, "state_indices", N, ())
+    _whole(initial_state, "state pool" if pool else "initial_state", sd, 1 if pool else N, one)
+    _whole(state_indices, "state_indices", torch.int32, N, ())
     dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, initial_state, state_indices))
     desc.num_slots = initial_state.shape[0] if pool else 0
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
     final = initial_state if pool else (torch.empty(N, *one, dtype=sd, device=dev) if output_final_state else None)
-    with torch.cuda.device(dev):
-        nbytes = int(lib().kda_ssm_prefill_workspace_size(ctypes.byref(desc)))
-        ws = _scratch(nbytes, dev) if nbytes else None
-        _check(lib().kda_ssm_prefill(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                     _ptr(dt_bias), _ptr(cu_seqlens), _ptr(initial_state), _ptr(state_indices),
-                                     None if pool else _ptr(final), _ptr(y), _ptr(ws), nbytes, _stream(dev)))
+    nbytes = lib().kda_ssm_prefill_workspace_size(ctypes.byref(desc))
+    ws = _scratch(nbytes, dev) if nbytes else None
+    _launch(dev, lib().kda_ssm_prefill, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+            _ptr(dt_bias), _ptr(cu_seqlens), _ptr(initial_state), _ptr(state_indices), None if pool else _ptr(final), _ptr(y), _ptr(ws),
+            nbytes)
     return y, final
 
 
 def ssm_decode(x, dt, A_log, B, C, state_pool, state_indices, *, D=None, z=None, dt_bias=None):
     """One token of every request through the scan, in place on the pool
     [slots, H, P, S].  Returns y [B, H, P]."""
-    _need(state_pool, "state_pool", None, 4)
-    _need(state_indices, "state_indices", torch.int32, 1)
-    desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, x.shape[0], state_pool.dtype)
-    _rows(state_pool, "state_pool", 1, (desc.heads, desc.head_dim, desc.state_dim))
-    _rows(state_indices, "state_indices", x.shape[0], ())
+    n = x.shape[0]
+    desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, n, state_pool.dtype)
+    _whole(state_pool, "state_pool", state_pool.dtype, 1, (desc.heads, desc.head_dim, desc.state_dim))
+    _whole(state_indices, "state_indices", torch.int32, n, ())
     dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, state_pool, state_indices))
     desc.num_slots = state_pool.shape[0]
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().kda_ssm_decode(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                    _ptr(dt_bias), _ptr(state_pool), _ptr(state_indices), _ptr(y), _stream(dev)))
+    _launch(dev, lib().kda_ssm_decode, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+            _ptr(dt_bias), _ptr(state_pool), _ptr(state_indices), _ptr(y))
     return y
 
 
@@ -756,22 +778,19 @@ def ssm_decode_multi(x, dt, A_log, B, C, cu_seqlens, state_pool, state_indices, 
     S], rows beyond `steps` not kept), the last one to the pool row with
     update_pool.  Returns y [T, H, P]."""
     N = _cu(cu_seqlens)
-    _need(state_pool, "state_pool", None, 4)
-    _need(state_indices, "state_indices", torch.int32, 1)
     desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, N, state_pool.dtype)
     one = (desc.heads, desc.head_dim, desc.state_dim)
-    _rows(state_pool, "state_pool", 1, one)
-    _rows(state_indices, "state_indices", N, ())
+    _whole(state_pool, "state_pool", state_pool.dtype, 1, one)
+    _whole(state_indices, "state_indices", torch.int32, N, ())
     desc.cache_pitch = _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
     dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, state_pool, state_indices, intermediate_states))
     desc.num_slots = state_pool.shape[0]
     desc.cache_steps = 0 if intermediate_states is None else intermediate_states.shape[1]
     desc.update_pool = 1 if update_pool else 0
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().kda_ssm_decode_multi(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                          _ptr(dt_bias), _ptr(cu_seqlens), _ptr(state_pool), _ptr(state_indices),
-                                          _ptr(intermediate_states) if desc.cache_steps else None, _ptr(y), _stream(dev)))
+    _launch(dev, lib().kda_ssm_decode_multi, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+            _ptr(dt_bias), _ptr(cu_seqlens), _ptr(state_pool), _ptr(state_indices),
+            _ptr(intermediate_states) if desc.cache_steps else None, _ptr(y))
     return y
 
 
@@ -792,21 +811,17 @@ def verify_drafts(tokens, target_probs, cu_seqlens, uniform, uniform_next, *, dr
     N, T, V = _cu(cu_seqlens), tokens.shape[0], target_probs.shape[1]
     pitch = _token_rows(target_probs, "target_probs", target_probs.dtype, T, (V,))
     draft_pitch = 0 if draft_probs is None else _token_rows(draft_probs, "draft_probs", target_probs.dtype, T, (V,))
-    _need(uniform, "uniform", torch.float32, 1)
-    _need(uniform_next, "uniform_next", torch.float32, 1)
-    _rows(uniform, "uniform", T, ())
-    _rows(uniform_next, "uniform_next", N, ())
+    _whole(uniform, "uniform", torch.float32, T, ())
+    _whole(uniform_next, "uniform_next", torch.float32, N, ())
     dev = _on_device(target_probs, (tokens, cu_seqlens, uniform, uniform_next, draft_probs))
     desc = VerifyDesc(N, T, V, _DT[target_probs.dtype], pitch, draft_pitch)
     accepted = torch.empty(N, dtype=torch.int32, device=dev)
     next_tokens = torch.empty(N, dtype=torch.int32, device=dev)
     emitted = torch.empty(T, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        nbytes = int(lib().kda_verify_drafts_workspace_size(ctypes.byref(desc)))
-        ws = _scratch(nbytes, dev)
-        _check(lib().kda_verify_drafts(ctypes.byref(desc), _ptr(tokens), _ptr(target_probs), _ptr(draft_probs), _ptr(cu_seqlens),
-                                       _ptr(uniform), _ptr(uniform_next), _ptr(accepted), _ptr(next_tokens), _ptr(emitted), _ptr(ws),
-                                       ws.numel(), _stream(dev)))
+    nbytes = lib().kda_verify_drafts_workspace_size(ctypes.byref(desc))
+    ws = _scratch(nbytes, dev)
+    _launch(dev, lib().kda_verify_drafts, ctypes.byref(desc), _ptr(tokens), _ptr(target_probs), _ptr(draft_probs), _ptr(cu_seqlens),
+            _ptr(uniform), _ptr(uniform_next), _ptr(accepted), _ptr(next_tokens), _ptr(emitted), _ptr(ws), max(nbytes, 16))
     return accepted, next_tokens, emitted
 
 
@@ -814,18 +829,16 @@ def commit_states(state_pool, state_indices, intermediate_states, steps):
     """state_pool[state_indices[n]] = intermediate_states[n, steps[n]]: the
     accepted step of a verify decode's cache becomes the request's state
     (negative steps, or steps the cache does not hold: left as it is)."""
-    _need(state_pool, "state_pool", None, 4)
-    _need(state_indices, "state_indices", torch.int32, 1)
-    _need(steps, "steps", torch.int32, 1)
-    N = steps.shape[0]
-    _rows(state_pool, "state_pool", 1, tuple(state_pool.shape[1:]))
-    _rows(state_indices, "state_indices", N, ())
+    if state_pool.dim() != 4 or steps.dim() != 1:
+        raise ValueError("state_pool must be [slots, H, V, K] and steps [N]")
+    N, one = steps.shape[0], tuple(state_pool.shape[1:])
+    _whole(steps, "steps", torch.int32, N, ())
+    _whole(state_pool, "state_pool", state_pool.dtype, 1, one)
+    _whole(state_indices, "state_indices", torch.int32, N, ())
     if intermediate_states is None:
         raise ValueError("commit_states needs the step cache")
-    pitch = _cache_pitch(intermediate_states, N, *state_pool.shape[1:], state_pool.dtype)
+    pitch = _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
     dev = _on_device(state_pool, (state_indices, intermediate_states, steps))
-    desc = CommitDesc(N, state_pool.shape[0], intermediate_states.shape[1], pitch,
-                      state_pool[0].numel() * state_pool.element_size())
-    with torch.cuda.device(dev):
-        _check(lib().kda_commit_states(ctypes.byref(desc), _ptr(state_pool), _ptr(state_indices), _ptr(intermediate_states),
-                                       _ptr(steps), _stream(dev)))
+    desc = CommitDesc(N, state_pool.shape[0], intermediate_states.shape[1], pitch, one[0] * one[1] * one[2] * state_pool.element_size())
+    _launch(dev, lib().kda_commit_states, ctypes.byref(desc), _ptr(state_pool), _ptr(state_indices), _ptr(intermediate_states),
+            _ptr(steps))

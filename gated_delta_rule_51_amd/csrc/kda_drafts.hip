@@ -3,25 +3,32 @@
 //
 // A request's drafts are tested 64 at a time, one a lane; the first refused
 // one gives the row whose rest the next token is drawn from.  That row (and
-// the drafts' own, where one was refused) is read once: wave-sized parts are
-// summed in fp64, the part that holds r times the total is found from the
-// sums, and only that part is read again to find the token.  Bound by those
-// rows' bytes with many requests, by the chain of dependent loads with one.
+// the drafts' own, where one was refused) is read once, in parts of a few
+// thousand tokens summed by a wave in fp64; the part that holds r times the
+// total is found from the sums, and only that part is read again to find the
+// token.  Bound by those rows' bytes with many requests, by the chain of
+// dependent loads with one.
 #include "kda_device.h"
 #include "kda_internal.h"
 
 namespace kda {
 
-constexpr int kVerifyWaves = 8;                    // waves (parts) of a workgroup
+constexpr int kVerifyWaves = 8;
 constexpr int kVerifyThreads = kVerifyWaves * 64;
 constexpr int kVerifyParts = 256;                  // most parts of a row
+constexpr int kVec = 4;                            // neighbouring tokens of a lane
+constexpr int kPart = 4 * 64 * kVec;               // tokens of a part: a multiple of this
 
-// Parts a row is summed in.  One workgroup's waves where the requests fill the
-// chip by themselves; else more workgroups a row, no part below 1024 tokens.
-int verify_parts(int num_seqs, int vocab) {
-    int parts = kVerifyWaves;
-    while (parts < kVerifyParts && (long)num_seqs * parts < 4096 && vocab / (2 * parts) >= 1024) parts *= 2;
-    return parts;
+static int part_tokens(int vocab) {
+    return (int)((((long)vocab + kVerifyParts - 1) / kVerifyParts + kPart - 1) / kPart * kPart);
+}
+int verify_parts(int, int vocab) { return (int)(((long)vocab + part_tokens(vocab) - 1) / part_tokens(vocab)); }
+
+// Workgroups a row's parts are summed by: one, which then finds the token as
+// well, where the requests fill the chip by themselves, else a wave a part.
+// Measured at V = 65,536 (64 parts), one and eight: see the launch below.
+static int verify_groups(int num_seqs, int parts) {
+    return num_seqs >= 256 ? 1 : (parts + kVerifyWaves - 1) / kVerifyWaves;
 }
 
 struct Verdict {
@@ -62,14 +69,32 @@ template <typename PT> __device__ __forceinline__ Verdict judge(const VerifyArgs
     return v;
 }
 
-// The weight of token i in the refused row (or the last one), and p itself.
+// The refused (or last) row: weights w and p's own.
 template <typename PT> struct Row {
     const PT *p, *q;   // q: NULL where nothing is taken off
     int wrong;         // token of weight 0, or -1
-    __device__ __forceinline__ void at(int i, float &w, float &own) const {
-        const float x = io_traits<PT>::load(p, i);
-        own = fmaxf(x, 0.f);   // NaN weighs nothing
-        w = q ? fmaxf(x - io_traits<PT>::load(q, i), 0.f) : i == wrong ? 0.f : own;
+    int vocab;
+    bool wide;         // rows start on 16 (bf16: 8) bytes
+
+    // Tokens i .. i + 3; those past the vocabulary weigh nothing.
+    __device__ __forceinline__ void at(int i, float (&w)[kVec], float (&own)[kVec]) const {
+        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+        if (wide && i + kVec <= vocab) {
+            x = load4(p + i);
+            if (q) y = load4(q + i);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                if (i + e < vocab) {
+                    x[e] = io_traits<PT>::load(p, i + e);
+                    if (q) y[e] = io_traits<PT>::load(q, i + e);
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            own[e] = fmaxf(x[e], 0.f);   // NaN weighs nothing
+            w[e] = q ? fmaxf(x[e] - y[e], 0.f) : i + e == wrong ? 0.f : own[e];
+        }
     }
 };
 
@@ -79,105 +104,130 @@ template <typename PT> __device__ __forceinline__ Row<PT> row_of(const VerifyArg
     r.p = reinterpret_cast<const PT *>(a.target) + t * a.target_stride;
     r.q = a.draft && v.refused ? reinterpret_cast<const PT *>(a.draft) + t * a.draft_stride : nullptr;
     r.wrong = v.refused ? v.wrong : -1;
+    r.vocab = a.vocab;
+    r.wide = a.target_stride % kVec == 0 && a.draft_stride % kVec == 0;
     return r;
 }
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
-    return x;
-}
-
-// Range of part k of `parts`: whole multiples of 64 tokens but for the last.
-__device__ __forceinline__ void part_range(int vocab, int parts, int k, int &lo, int &hi) {
-    const int each = ((vocab + parts - 1) / parts + 63) / 64 * 64;
-    lo = (int)min((long)vocab, (long)each * k);
-    hi = (int)min((long)vocab, (long)lo + each);
-}
-
+// A wave's sums of one part: of the weights and of p.
 template <typename PT>
 __device__ __forceinline__ void sum_part(const Row<PT> &r, int lo, int hi, int lane, double &w, double &own) {
     w = 0.0;
     own = 0.0;
-    for (int i = lo + lane; i < hi; i += 64) {
-        float x, o;
-        r.at(i, x, o);
-        w += (double)x;
-        own += (double)o;
+    for (int base = lo; base < hi; base += kPart) {
+#pragma unroll
+        for (int k = 0; k < kPart / (64 * kVec); ++k) {
+            float x[kVec], o[kVec];
+            r.at(base + (k * 64 + lane) * kVec, x, o);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                w += (double)x[e];
+                own += (double)o[e];
+            }
+        }
     }
-    w = wave_sum(w);
-    own = wave_sum(own);
+    w = lane_value(wave_scan(w), 63);
+    own = lane_value(wave_scan(own), 63);
 }
 
-// The whole workgroup: the sums of all parts are in sums[0][..] (weights) and
-// sums[1][..] (p); writes the request's outputs.
-template <typename PT>
-__device__ void pick(const VerifyArgs &a, int n, const Verdict &v, const Row<PT> &r, const double *sums, double *scan) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int parts = a.parts;
-    __shared__ int found;
-    // every thread walks the sums alike: no part to agree on
-    double total = 0.0;
-    for (int k = 0; k < parts; ++k) total += sums[k];
-    const bool rest = total > 0.0;
-    if (!rest) {
-        total = 0.0;
-        for (int k = 0; k < parts; ++k) total += sums[parts + k];
-    }
-    const double *s = rest ? sums : sums + parts;
-    const double want = (double)a.uniform_next[n] * total;
-    double before = 0.0, cum = 0.0;
-    int part = -1;
-    for (int k = 0; k < parts; ++k) {
-        if (s[k] > 0.0) {   // the last part with any weight where none reaches past `want`
-            part = k;
-            before = cum;
-        }
-        cum += s[k];
-        if (cum > want) break;
-    }
-    if (tid == 0) found = -1;
-    __syncthreads();
-    if (part >= 0) {
-        int lo, hi;
-        part_range(a.vocab, parts, part, lo, hi);
-        double carry = before;
-        for (int base = lo; base < hi; base += kVerifyThreads) {
-            const int i = base + tid;
-            float w = 0.f, own = 0.f;
-            if (i < hi) r.at(i, w, own);
-            const double x = rest ? (double)w : (double)own;
-            double c = x;
+// The part of a row that holds `want` = r times the total, from the sums of
+// all parts (every wave finds the same): its number, or -1 where no part has
+// any weight, and the sum before it.
+__device__ __forceinline__ int find_part(const double *sums, int parts, float r, int lane, double &want, double &before) {
+    constexpr int EACH = kVerifyParts / 64;
+    double s[EACH], own = 0.0;
 #pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const double y = __shfl_up(c, m, 64);
-                if (lane >= m) c += y;
+    for (int k = 0; k < EACH; ++k) {
+        const int i = lane * EACH + k;
+        s[k] = i < parts ? sums[i] : 0.0;
+        own += s[k];
+    }
+    const double cum = wave_scan(own), total = lane_value(cum, 63);
+    want = (double)r * total;
+    double c = cum - own, at = 0.0;
+    int hit = -1, last = -1;   // first part past `want`; the last with any weight where rounding (or r = 1) leaves none
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        if (s[k] > 0.0) {
+            last = lane * EACH + k;
+            if (hit < 0) {
+                at = c;
+                if (c + s[k] > want) hit = last;
             }
-            if (lane == 63) scan[wave] = c;
+        }
+        c += s[k];
+    }
+    const unsigned long long past = __ballot(hit >= 0), some = __ballot(last >= 0);
+    if (!some) return -1;
+    const int from = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+    before = lane_value(at, from);
+    return __builtin_amdgcn_readlane(past ? hit : last, from);
+}
+
+// The whole workgroup: finds the token and writes the request's outputs.
+// sums: of the weights of all parts, then of p of all parts.
+template <typename PT>
+__device__ void pick(const VerifyArgs &a, int n, const Verdict &v, const Row<PT> &r, const double *sums, int part_len) {
+    __shared__ double totals[kVerifyWaves];
+    __shared__ int hits[kVerifyWaves], lasts[kVerifyWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    double want = 0.0, carry = 0.0;
+    bool rest = true;
+    int part = find_part(sums, a.parts, a.uniform_next[n], lane, want, carry), next = -1;
+    if (part < 0) {   // nothing is left of the row: p itself
+        rest = false;
+        part = find_part(sums + a.parts, a.parts, a.uniform_next[n], lane, want, carry);
+    }
+    if (part >= 0) {
+        const int lo = part * part_len, hi = (int)min((long)a.vocab, (long)lo + part_len);
+        for (int base = lo; base < hi; base += kVerifyThreads * kVec) {
+            const int i = base + tid * kVec;
+            float x[kVec], o[kVec];
+            r.at(i, x, o);
+            double own = 0.0;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                x[e] = i + e >= hi ? 0.f : rest ? x[e] : o[e];
+                own += (double)x[e];
+            }
+            const double cum = wave_scan(own);
+            if (lane == 63) totals[wave] = cum;
             __syncthreads();
-            double off = carry;
-            for (int k = 0; k < wave; ++k) off += scan[k];
-            for (int k = 0; k < kVerifyWaves; ++k) carry += scan[k];
-            // the first token past `want`; failing that (rounding, or a random
-            // number of 1) the last token with any weight
-            const unsigned long long past = __ballot(x > 0.0 && off + c > want);
-            if (past && lane == 0) scan[kVerifyWaves + wave] = (double)(base + wave * 64 + __builtin_ctzll(past));
-            else if (lane == 0) scan[kVerifyWaves + wave] = -1.0;
-            const unsigned long long some = __ballot(x > 0.0);
-            if (lane == 0) scan[2 * kVerifyWaves + wave] = some ? (double)(base + wave * 64 + 63 - __builtin_clzll(some)) : -1.0;
-            __syncthreads();
-            int hit = -1, last = -1;
+            double c = carry + (cum - own);
+#pragma unroll
             for (int k = 0; k < kVerifyWaves; ++k) {
-                if (hit < 0 && scan[kVerifyWaves + k] >= 0.0) hit = (int)scan[kVerifyWaves + k];
-                if (scan[2 * kVerifyWaves + k] >= 0.0) last = (int)scan[2 * kVerifyWaves + k];
+                if (k < wave) c += totals[k];
+                carry += totals[k];
             }
-            if (tid == 0 && (hit >= 0 || last >= 0)) found = hit >= 0 ? hit : last;
+            // the first token past `want`; failing that the last with any weight
+            int hit = -1, last = -1;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                c += (double)x[e];
+                if (x[e] > 0.f) {
+                    last = i + e;
+                    if (hit < 0 && c > want) hit = i + e;
+                }
+            }
+            const unsigned long long past = __ballot(hit >= 0), some = __ballot(last >= 0);
+            hit = past ? __builtin_amdgcn_readlane(hit, __builtin_ctzll(past)) : -1;
+            last = some ? __builtin_amdgcn_readlane(last, 63 - __builtin_clzll(some)) : -1;
+            if (lane == 0) {
+                hits[wave] = hit;
+                lasts[wave] = last;
+            }
             __syncthreads();
+            hit = -1;
+#pragma unroll
+            for (int k = 0; k < kVerifyWaves; ++k) {
+                if (hit < 0) hit = hits[k];
+                if (lasts[k] >= 0) last = lasts[k];
+            }
+            if (hit >= 0 || last >= 0) next = hit >= 0 ? hit : last;
+            __syncthreads();   // before the next tokens' totals and hits
             if (hit >= 0) break;
         }
     }
-    __syncthreads();
-    const int next = found;
     if (tid == 0) {
         a.accepted[n] = v.accepted;
         a.next[n] = next;
@@ -186,10 +236,13 @@ __device__ void pick(const VerifyArgs &a, int n, const Verdict &v, const Row<PT>
         a.emitted[v.t0 + j] = j < v.accepted ? a.tokens[v.t0 + j + 1] : j == v.accepted ? next : -1;
 }
 
+// What the first launch leaves for the second: [N] verdicts, then the sums.
+struct Left { int accepted, wrong; };
+
 // grid (workgroups of a row, requests on y and z): sums the parts; with one
 // workgroup a row also finds the token.
-template <typename PT> __global__ __launch_bounds__(kVerifyThreads) void verify_sum_kernel(VerifyArgs a) {
-    __shared__ double sums[2 * kVerifyWaves], scan[3 * kVerifyWaves];
+template <typename PT> __global__ __launch_bounds__(kVerifyThreads) void verify_sum_kernel(VerifyArgs a, int part_len) {
+    __shared__ double sums[2 * kVerifyParts];
     const int n = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (n >= a.num_seqs) return;
@@ -201,45 +254,46 @@ template <typename PT> __global__ __launch_bounds__(kVerifyThreads) void verify_
         }
         return;
     }
+    const bool alone = gridDim.x == 1;
+    double *out = alone ? sums : a.partial + a.num_seqs + (long)n * 2 * a.parts;
+    if (!alone && blockIdx.x == 0 && threadIdx.x == 0) reinterpret_cast<Left *>(a.partial)[n] = Left{v.accepted, v.wrong};
     const Row<PT> r = row_of<PT>(a, v);
-    const int part = (int)blockIdx.x * kVerifyWaves + wave;
-    int lo, hi;
-    part_range(a.vocab, a.parts, part, lo, hi);
-    double w, own;
-    sum_part<PT>(r, lo, hi, lane, w, own);
-    if (gridDim.x > 1) {
+    for (int part = (int)blockIdx.x * kVerifyWaves + wave; part < a.parts; part += (int)gridDim.x * kVerifyWaves) {
+        double w, own;
+        const int lo = part * part_len;
+        sum_part<PT>(r, lo, (int)min((long)a.vocab, (long)lo + part_len), lane, w, own);
         if (lane == 0) {
-            a.partial[((long)n * 2) * a.parts + part] = w;
-            a.partial[((long)n * 2 + 1) * a.parts + part] = own;
+            out[part] = w;
+            out[a.parts + part] = own;
         }
-        return;
     }
-    if (lane == 0) {
-        sums[wave] = w;
-        sums[kVerifyWaves + wave] = own;
-    }
+    if (!alone) return;
     __syncthreads();
-    pick<PT>(a, n, v, r, sums, scan);
+    pick<PT>(a, n, v, r, sums, part_len);
 }
 
 // grid (1, requests on y and z): the token from the parts' sums.
-template <typename PT> __global__ __launch_bounds__(kVerifyThreads) void verify_pick_kernel(VerifyArgs a) {
-    __shared__ double sums[2 * kVerifyParts], scan[3 * kVerifyWaves];
+template <typename PT> __global__ __launch_bounds__(kVerifyThreads) void verify_pick_kernel(VerifyArgs a, int part_len) {
     const int n = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
     if (n >= a.num_seqs) return;
-    for (int k = threadIdx.x; k < 2 * a.parts; k += kVerifyThreads) sums[k] = a.partial[(long)n * 2 * a.parts + k];
-    const Verdict v = judge<PT>(a, n, threadIdx.x & 63);
+    Verdict v;
+    v.t0 = a.cu_seqlens[n];
+    v.len = a.cu_seqlens[n + 1] - v.t0;
     if (v.len <= 0) return;
-    __syncthreads();
-    pick<PT>(a, n, v, row_of<PT>(a, v), sums, scan);
+    const Left left = reinterpret_cast<const Left *>(a.partial)[n];
+    v.accepted = left.accepted;
+    v.wrong = left.wrong;
+    v.refused = v.accepted < v.len - 1;
+    pick<PT>(a, n, v, row_of<PT>(a, v), a.partial + a.num_seqs + (long)n * 2 * a.parts, part_len);
 }
 
 template <typename PT> static hipError_t launch_p(const VerifyArgs &a, hipStream_t s) {
-    const dim3 grid(a.parts / kVerifyWaves, decode_grid_y(a.num_seqs), decode_grid_z(a.num_seqs));
-    verify_sum_kernel<PT><<<grid, kVerifyThreads, 0, s>>>(a);
+    const dim3 grid(verify_groups(a.num_seqs, a.parts), decode_grid_y(a.num_seqs), decode_grid_z(a.num_seqs));
+    const int part_len = part_tokens(a.vocab);
+    verify_sum_kernel<PT><<<grid, kVerifyThreads, 0, s>>>(a, part_len);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || grid.x == 1) return e;
-    verify_pick_kernel<PT><<<dim3(1, grid.y, grid.z), kVerifyThreads, 0, s>>>(a);
+    verify_pick_kernel<PT><<<dim3(1, grid.y, grid.z), kVerifyThreads, 0, s>>>(a, part_len);
     return hipGetLastError();
 }
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t s) { return a.bf16 ? launch_p<bf16>(a, s) : launch_p<float>(a, s); }

@@ -100,7 +100,7 @@ struct VerifyArgs {
     const void *target, *draft;
     const float *uniform, *uniform_next;
     int32_t *accepted, *next, *emitted;
-    double *partial;             // [N, 2, parts] sums, or NULL with one part
+    double *partial;             // [N] verdicts (8 bytes each), then [N, 2, parts] sums
     int num_seqs, vocab, parts;
     bool bf16;
     long target_stride, draft_stride;

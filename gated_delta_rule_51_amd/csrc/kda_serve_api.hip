@@ -323,7 +323,7 @@ kda_status kda_ssm_decode_multi(const kda_ssm_desc *d, const void *x, const void
 
 size_t kda_verify_drafts_workspace_size(const kda_verify_desc *d) {
     if (check_verify(d) != KDA_OK) return 0;
-    return (size_t)d->num_seqs * 2 * verify_parts(d->num_seqs, d->vocab) * sizeof(double);
+    return (size_t)d->num_seqs * (1 + 2 * (size_t)verify_parts(d->num_seqs, d->vocab)) * sizeof(double);
 }
 
 kda_status kda_verify_drafts(const kda_verify_desc *d, const int32_t *tokens, const void *target_probs, const void *draft_probs,

@@ -128,26 +128,6 @@ __device__ __forceinline__ void m_part(const f32x16 &cb, const float *gate, int 
     }
 }
 
-// Inclusive sums over the wave's lanes, without a trip through LDS.
-template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_add(double x) {
-    const u32x2 w = __builtin_bit_cast(u32x2, x);
-    return x + __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xf, false),
-                                                (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xf, false)});
-}
-__device__ __forceinline__ double wave_scan(double x) {
-    x = dpp_add<0x111, 0xf>(x);   // from 1, 2, 4 and 8 lanes below within a row of 16
-    x = dpp_add<0x112, 0xf>(x);
-    x = dpp_add<0x114, 0xf>(x);
-    x = dpp_add<0x118, 0xf>(x);
-    x = dpp_add<0x142, 0xa>(x);   // a row's last lane to the next row
-    return dpp_add<0x143, 0xc>(x);   // lane 31 to the upper half
-}
-__device__ __forceinline__ double lane_value(double x, int lane) {
-    const u32x2 w = __builtin_bit_cast(u32x2, x);
-    return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)w[0], lane),
-                                            (uint32_t)__builtin_amdgcn_readlane((int)w[1], lane)});
-}
-
 struct Segments {
     int len;        // tokens, a multiple of 64
     int slots;      // floor(T / len) + N
