@@ -79,8 +79,8 @@ kda_status check_ssm(const kda_ssm_desc *d, bool pool) {
     const long hp = (long)d->heads * d->head_dim, gs = (long)d->groups * d->state_dim;
     if (d->x_stride < hp || d->dt_stride < d->heads || d->b_stride < gs || d->c_stride < gs || d->z_stride < 0) return KDA_ERR_SHAPE;
     // 64 rows stay within a buffer resource's 31 bits
-    const int64_t far = 1 << 23;
-    if (d->x_stride > far || d->b_stride > far || d->c_stride > far) return KDA_ERR_UNSUPPORTED;
+    const int64_t far = 1 << 22;
+    if (d->x_stride > far || d->b_stride > far || d->c_stride > far || d->z_stride > far) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -219,8 +219,7 @@ kda_status kda_conv_commit(const kda_conv_desc *d, const void *x, const int32_t 
 
 size_t kda_ssm_prefill_workspace_size(const kda_ssm_desc *d) {
     if (check_ssm(d, false) != KDA_OK) return 0;
-    return ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim, d->state_dim,
-                                       d->io_dtype == KDA_BF16);
+    return ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim, d->state_dim);
 }
 
 kda_status kda_ssm_prefill(const kda_ssm_desc *d, const void *x, const void *dt, const float *A_log, const void *B, const void *C,
@@ -233,8 +232,7 @@ kda_status kda_ssm_prefill(const kda_ssm_desc *d, const void *x, const void *dt,
     const long T = d->total_tokens, N = d->num_seqs;
     if (!cu_seqlens || (pool && !state)) return KDA_ERR_NULL;
     if (pool && final_state && final_state != state) return KDA_ERR_ALIAS;
-    const size_t need = ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim, d->state_dim,
-                                                    d->io_dtype == KDA_BF16);
+    const size_t need = ssm_prefill_workspace_bytes(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim, d->state_dim);
     const Range before{state, ssm_states(d, pool ? d->num_slots : N)}, last{pool ? nullptr : final_state, ssm_states(d, N)};
     const Range more[5] = {before, last, {cu_seqlens, (size_t)(N + 1) * 4}, {state_indices, (size_t)N * 4}, {workspace, need}};
     SsmArgs a;

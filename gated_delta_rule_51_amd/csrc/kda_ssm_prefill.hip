@@ -1,4 +1,5 @@
-// Selective state-space scan of packed prompts, bf16 io, in chunks of 64
+// Selective state-space scan of packed prompts (bf16 io; the launches of both
+// kinds), in chunks of 64
 // tokens on the matrix cores.
 //
 // With G_t the running sum of log-decays within a chunk, S the state before it:
@@ -35,13 +36,10 @@
 // one or two segments thus do no work twice.
 #include <type_traits>
 
-#include "kda_device.h"
-#include "kda_internal.h"
-#include "kda_ssm.h"
+#include "kda_ssm_chunk.h"
 
 namespace kda {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -76,18 +74,6 @@ template <int TERMS> __device__ __forceinline__ void split(const float (&v)[8], 
     }
 }
 
-// A value (of 8 bytes) all lanes share, in scalar registers.
-template <typename T> __device__ __forceinline__ T uniform(T x) {
-    static_assert(sizeof(T) == 8, "two registers");
-    const u32x2 w = __builtin_bit_cast(u32x2, x);
-    return __builtin_bit_cast(T, u32x2{(uint32_t)__builtin_amdgcn_readfirstlane((int)w[0]),
-                                       (uint32_t)__builtin_amdgcn_readfirstlane((int)w[1])});
-}
-
-// Per token of a chunk: 0 and 1 the two floats of G (in powers of 2), 2 dt
-// over the decay of the second, 3 exp(G_last - G) dt, 4 exp(G).
-constexpr int kGateArrays = 5;
-
 template <int P, int S> struct Chunk {
     static constexpr int WPH = P / 32;          // waves of a head
     static constexpr int HW = 4 / WPH;          // heads of a workgroup
@@ -113,53 +99,16 @@ template <int PPR> __device__ __forceinline__ int tile_at(int row, int piece) {
     return row * PPR * 16 + ((piece ^ swizzle<PPR>(row & 15)) << 4);   // repeats every 16 rows
 }
 
-// Four columns of M's tile (rows t of 32 tt, columns s of 32 ss) from the
-// products C_t . B_s: registers 4q .. 4q + 3.  Every pair has its own
-// exponential, as a factor to a common point would overflow.
-__device__ __forceinline__ void m_part(const f32x16 &cb, const float *gate, int tt, int ss, int q, int lane, float Dh, float gt,
-                                       float lt, float (&v)[4]) {
-    const int t = 32 * tt + (lane & 31), s0 = 32 * ss + 8 * q + 4 * (lane >> 5);
-    const f32x4 gs = *reinterpret_cast<const f32x4 *>(gate + s0), ds = *reinterpret_cast<const f32x4 *>(gate + 128 + s0);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        float x = cb[4 * q + b] * (__builtin_amdgcn_exp2f((gt - gs[b]) + lt) * ds[b]);
-        x = s0 + b == t ? x + Dh : x;
-        v[b] = s0 + b <= t ? x : 0.f;
-    }
-}
-
-struct Segments {
-    int len;        // tokens, a multiple of 64
-    int slots;      // floor(T / len) + N
-    bool later;     // the last launch
-    float *states;  // [slots, H, P, S]: after the segment; before the next one once carried
-    float *decays;  // [slots, H]
-};
-
 template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmArgs a, Segments sg) {
     using C = Chunk<P, S>;
     extern __shared__ __align__(16) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int hs = wave / C::WPH, pc = wave % C::WPH;   // head of the workgroup, 32-column block of the head
 
-    const int rep = a.heads / a.groups, blocks = (rep + C::HW - 1) / C::HW;
-    const int sl = (int)blockIdx.x / (a.groups * blocks), rest = (int)blockIdx.x % (a.groups * blocks);
-    const int g = rest / blocks, first = g * rep + rest % blocks * C::HW;   // first head
-    const int h = first + hs;
-    const bool active = h < (g + 1) * rep;
-    const int seq = __builtin_amdgcn_readfirstlane(sg.slots == a.num_seqs ? sl : slot_sequence(a.cu_seqlens, a.num_seqs, sl, sg.len));
-    const int begin = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq]);
-    const int whole = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq + 1]) - begin;
-    const int local = sg.slots == a.num_seqs ? 0 : sl - (begin / sg.len + seq);   // segment of the sequence
-    const int segs = max(1, (whole + sg.len - 1) / sg.len);
-    if (local >= segs || (Y ? sg.later != (local > 0) : local == 0 || local == segs - 1)) return;
-    const int t0 = begin + local * sg.len, len = min(sg.len, whole - local * sg.len);
-    if (len <= 0 && (a.indices || !a.state_out)) return;
-    long slot = seq;
-    if (a.indices) {
-        slot = a.indices[seq];
-        if (slot < 0) slot = a.num_slots - 1;
-    }
+    const Place at(a, sg, C::HW, Y);
+    if (at.skip) return;
+    const int g = at.g, first = at.first, h = first + hs, t0 = at.t0, len = at.len;
+    const bool active = h < at.last;
 
     // state: register 8u + 4k + b of tile nt is column n = 32 nt + 16 u + 8 hh + 4 k + b of row pcol
     const auto in_heads = [&](int l) {
@@ -175,11 +124,11 @@ template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2
         for (int u = 0; u < 2; ++u) {
             f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
             if (sg.later) {
-                const float *p = sg.states + (sl - 1) * one + in_head + 32 * nt + 16 * u;
+                const float *p = sg.states + (at.sl - 1) * one + in_head + 32 * nt + 16 * u;
                 x = load4(p);
                 y = load4(p + 4);
-            } else if (a.state_in && local == 0) {
-                const ST *p = reinterpret_cast<const ST *>(a.state_in) + slot * one + in_head + 32 * nt + 16 * u;
+            } else if (a.state_in && at.local == 0) {
+                const ST *p = reinterpret_cast<const ST *>(a.state_in) + at.row * one + in_head + 32 * nt + 16 * u;
                 x = load4(p);
                 y = load4(p + 4);
             }
@@ -209,7 +158,7 @@ template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2
     auto stage_x = [&](int c0, int lane, int q) {
         const int tid = 64 * wave + lane;
         const unsigned off = (unsigned)((tid / 16) * (int)a.x_stride + (tid % 16) * 8) * 2;
-        const bool in = first + (tid % 16) * 8 / P < (g + 1) * rep;   // the piece's head is there
+        const bool in = first + (tid % 16) * 8 / P < at.last;   // the piece's head is there
         xr[q] = __builtin_amdgcn_raw_buffer_load_b128(rows_at(xg, a.x_stride, c0 + 16 * q, 16), in ? off : 0x80000000u, 0, 0);
     };
     constexpr int each = 256 / C::PPR;   // rows of B and C a pass of the workgroup loads
@@ -252,15 +201,8 @@ template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2
     };
     auto make_gates = [&](int c0, int buf, int lane) {
         const float step = c0 + lane < len ? softplus_f(lo_f(dtv) + bias) : 0.f;
-        const double G = wave_scan((double)step * A), last = lane_value(G, 63);
-        through = uniform(through + last);
         float *q = reinterpret_cast<float *>(lds + C::OFF_G + buf * C::GBYTES) + hs * kGateArrays * 64 + lane;
-        const float gh = (float)G, gl = (float)(G - (double)gh);
-        q[0] = gh;
-        q[64] = gl;
-        q[128] = step * __builtin_amdgcn_exp2f(-gl);
-        q[192] = step * __builtin_amdgcn_exp2f((float)(last - G));
-        q[256] = __builtin_amdgcn_exp2f(gh);
+        through = uniform(through + write_gates(q, step, A));
     };
 
     if (len > 0) {
@@ -541,9 +483,9 @@ template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2
         __syncthreads();   // every wave has read this chunk
     }
 
-    const bool last = local == segs - 1;   // else the state goes to the segment's place
+    const bool last = at.local == at.segs - 1;   // else the state goes to the segment's place
     if (!active || (last ? !a.state_out : sg.later)) return;
-    if (!last && gates && lane == 0) sg.decays[(long)sl * a.heads + h] = __builtin_amdgcn_exp2f((float)through);
+    if (!last && gates && lane == 0) sg.decays[(long)at.sl * a.heads + h] = __builtin_amdgcn_exp2f((float)through);
     int again = lane;   // the offsets formed anew, not kept through the loop
     asm volatile("" : "+v"(again));
     const long out_head = in_heads(again);
@@ -555,12 +497,12 @@ template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e / 4][e % 4] = st[nt][8 * u + e];
             if (!last) {
-                float *p = sg.states + sl * one + out_head + 32 * nt + 16 * u;
+                float *p = sg.states + at.sl * one + out_head + 32 * nt + 16 * u;
                 *reinterpret_cast<f32x4 *>(p) = x[0];
                 *reinterpret_cast<f32x4 *>(p + 4) = x[1];
                 continue;
             }
-            ST *p = reinterpret_cast<ST *>(a.state_out) + slot * one + out_head + 32 * nt + 16 * u;
+            ST *p = reinterpret_cast<ST *>(a.state_out) + at.row * one + out_head + 32 * nt + 16 * u;
             if constexpr (sizeof(ST) == 4) {
                 *reinterpret_cast<f32x4 *>(p) = x[0];
                 *reinterpret_cast<f32x4 *>(p + 4) = x[1];
@@ -590,19 +532,40 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Segments sg) 
     }
 }
 
+template <int P, int S, typename ST> static hipError_t launch_chunk(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+    using C = Chunk<P, S>;
+    static_assert(C::LDS <= 163840, "LDS");
+    const auto kern = whole ? ssm_chunk_kernel<P, S, ST, true> : ssm_chunk_kernel<P, S, ST, false>;
+    const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+    if (e != hipSuccess) return e;
+    kern<<<dim3(sg.slots * ssm_head_workgroups(a)), 256, C::LDS, s>>>(a, sg);
+    return hipGetLastError();
+}
+template <int P, int S> static hipError_t launch_st(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+    return a.state_bf16 ? launch_chunk<P, S, bf16>(a, sg, whole, s) : launch_chunk<P, S, float>(a, sg, whole, s);
+}
+template <int P> static hipError_t launch_s(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+    switch (a.s) {
+    case 32: return launch_st<P, 32>(a, sg, whole, s);
+    case 64: return launch_st<P, 64>(a, sg, whole, s);
+    default: return launch_st<P, 128>(a, sg, whole, s);
+    }
+}
+static hipError_t launch_any(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+    if (!a.io_bf16) return launch_ssm_chunk_f32(a, sg, whole, s);
+    switch (a.p) {
+    case 32: return launch_s<32>(a, sg, whole, s);
+    case 64: return launch_s<64>(a, sg, whole, s);
+    default: return launch_s<128>(a, sg, whole, s);
+    }
+}
+
 // Tokens of a segment: as many as leave the chip's 512 resident workgroups
 // about two segments each, at least four chunks.
-static int segment_tokens(int num_seqs, int total_tokens, int wgs) {
-    const long len = ((long)total_tokens * wgs / 1024 + 63) / 64 * 64;
-    return (int)(len < 256 ? 256 : len);
-}
-static int head_workgroups(int heads, int groups, int p) {
-    const int hw = 128 / p, rep = heads / groups;
-    return groups * ((rep + hw - 1) / hw);
-}
-static Segments segments_of(int num_seqs, int total_tokens, int heads, int groups, int p) {
+static Segments segments_of(int num_seqs, int total_tokens, int head_workgroups) {
     Segments sg{};
-    sg.len = segment_tokens(num_seqs, total_tokens, head_workgroups(heads, groups, p));
+    const long len = ((long)total_tokens * head_workgroups / 1024 + 63) / 64 * 64;
+    sg.len = (int)(len < 256 ? 256 : len);
     if (sg.len >= total_tokens) {   // every sequence is one segment
         sg.len = (total_tokens + 64) / 64 * 64;
         sg.slots = num_seqs;
@@ -611,61 +574,35 @@ static Segments segments_of(int num_seqs, int total_tokens, int heads, int group
     }
     return sg;
 }
+static int head_workgroups(int heads, int groups, int p) {
+    const int hw = 128 / p, rep = heads / groups;
+    return groups * ((rep + hw - 1) / hw);
+}
+int ssm_head_workgroups(const SsmArgs &a) { return head_workgroups(a.heads, a.groups, a.p); }
 
-size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int groups, int p, int s, bool io_bf16) {
-    if (!io_bf16 || num_seqs <= 0) return 0;
-    const Segments sg = segments_of(num_seqs, total_tokens, heads, groups, p);
+size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int groups, int p, int s) {
+    if (num_seqs <= 0) return 0;
+    const Segments sg = segments_of(num_seqs, total_tokens, head_workgroups(heads, groups, p));
     if (sg.slots == num_seqs) return 0;
     return (size_t)sg.slots * heads * ((size_t)p * s + 1) * sizeof(float);
 }
 
-template <int P, int S, typename ST> static hipError_t launch_chunk(const SsmArgs &a, void *workspace, hipStream_t stream) {
-    using C = Chunk<P, S>;
-    static_assert(C::LDS <= 163840, "LDS");
-    Segments sg = segments_of(a.num_seqs, a.total_tokens, a.heads, a.groups, a.p);
-    const dim3 grid(sg.slots * head_workgroups(a.heads, a.groups, P));
-    const auto whole = ssm_chunk_kernel<P, S, ST, true>, alone = ssm_chunk_kernel<P, S, ST, false>;
-    hipError_t e;
-    if ((e = hipFuncSetAttribute((const void *)whole, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS)) != hipSuccess) return e;
-    if (sg.slots == a.num_seqs) {
-        whole<<<grid, 256, C::LDS, stream>>>(a, sg);
-        return hipGetLastError();
-    }
-    const size_t one = (size_t)a.heads * P * S;
+hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t stream) {
+    Segments sg = segments_of(a.num_seqs, a.total_tokens, ssm_head_workgroups(a));
+    if (sg.slots == a.num_seqs) return launch_any(a, sg, true, stream);
+    const size_t one = (size_t)a.heads * a.p * a.s;
     sg.states = static_cast<float *>(workspace);
     sg.decays = sg.states + sg.slots * one;
-    whole<<<grid, 256, C::LDS, stream>>>(a, sg);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipError_t e = launch_any(a, sg, true, stream);
+    if (e != hipSuccess) return e;
     if (2L * sg.len < a.total_tokens) {   // a sequence of three segments may be there
-        if ((e = hipFuncSetAttribute((const void *)alone, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS)) != hipSuccess) return e;
-        alone<<<grid, 256, C::LDS, stream>>>(a, sg);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if ((e = launch_any(a, sg, false, stream)) != hipSuccess) return e;
         ssm_carry_kernel<<<dim3((unsigned)((one / 4 + 255) / 256), decode_grid_y(a.num_seqs), decode_grid_z(a.num_seqs)), 256, 0,
                            stream>>>(a, sg);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     sg.later = true;
-    whole<<<grid, 256, C::LDS, stream>>>(a, sg);
-    return hipGetLastError();
-}
-template <int P, int S> static hipError_t launch_st(const SsmArgs &a, void *w, hipStream_t s) {
-    return a.state_bf16 ? launch_chunk<P, S, bf16>(a, w, s) : launch_chunk<P, S, float>(a, w, s);
-}
-template <int P> static hipError_t launch_s(const SsmArgs &a, void *w, hipStream_t s) {
-    switch (a.s) {
-    case 32: return launch_st<P, 32>(a, w, s);
-    case 64: return launch_st<P, 64>(a, w, s);
-    default: return launch_st<P, 128>(a, w, s);
-    }
-}
-
-hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t s) {
-    if (!a.io_bf16) return launch_ssm_run(a, s);
-    switch (a.p) {
-    case 32: return launch_s<32>(a, workspace, s);
-    case 64: return launch_s<64>(a, workspace, s);
-    default: return launch_s<128>(a, workspace, s);
-    }
+    return launch_any(a, sg, true, stream);
 }
 
 }  // namespace kda
