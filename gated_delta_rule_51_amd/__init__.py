@@ -560,11 +560,12 @@ def recurrent_decode_packed_fused_gate(qkv, gate_x, A_log, dt_bias, beta_x, stat
 # only then, where it does not hold, find out what to say.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(dev, fn, *args):
     """fn(*args, current stream of dev) with dev the current device."""
-    if torch.cuda.current_device() == dev.index:
+    if _get_device() == dev.index:
         _check(fn(*args, _raw_stream(dev.index) if _raw_stream else _stream(dev)))
     else:
         with torch.cuda.device(dev):
@@ -661,7 +662,7 @@ def conv_prefill(x, weight, bias, cu_seqlens, *, initial_state=None, state_indic
     _whole(state_indices, "state_indices", torch.int32, N, ())
     dev = _on_device(x, (weight, bias, cu_seqlens, initial_state, state_indices))
     desc = ConvDesc(N, T, D, W, dt, 1 if activation else 0, initial_state.shape[0] if pool else 0, 1 if update_pool else 0, stride)
-    y = torch.empty(T, D, dtype=x.dtype, device=dev)
+    y = x.new_empty((T, D))
     final = initial_state if pool else (torch.empty(N, W - 1, D, dtype=x.dtype, device=dev) if output_final_state else None)
     _launch(dev, lib().kda_conv_prefill, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(initial_state),
             _ptr(state_indices), None if pool else _ptr(final), _ptr(y))
@@ -678,7 +679,7 @@ def conv_decode(x, weight, bias, conv_pool, state_indices, *, activation="silu")
     _whole(state_indices, "state_indices", torch.int32, B, ())
     dev = _on_device(x, (weight, bias, conv_pool, state_indices))
     desc = ConvDesc(B, B, D, W, dt, 1 if activation else 0, conv_pool.shape[0], 1, stride)
-    y = torch.empty(B, D, dtype=x.dtype, device=dev)
+    y = x.new_empty((B, D))
     _launch(dev, lib().kda_conv_decode, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_pool), _ptr(state_indices),
             _ptr(y))
     return y
@@ -746,7 +747,7 @@ def ssm_prefill(x, dt, A_log, B, C, cu_seqlens, *, D=None, z=None, dt_bias=None,
     _whole(state_indices, "state_indices", torch.int32, N, ())
     dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, initial_state, state_indices))
     desc.num_slots = initial_state.shape[0] if pool else 0
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = x.new_empty(x.shape)
     final = initial_state if pool else (torch.empty(N, *one, dtype=sd, device=dev) if output_final_state else None)
     nbytes = lib().kda_ssm_prefill_workspace_size(ctypes.byref(desc))
     ws = _scratch(nbytes, dev) if nbytes else None
@@ -765,7 +766,7 @@ def ssm_decode(x, dt, A_log, B, C, state_pool, state_indices, *, D=None, z=None,
     _whole(state_indices, "state_indices", torch.int32, n, ())
     dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, state_pool, state_indices))
     desc.num_slots = state_pool.shape[0]
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = x.new_empty(x.shape)
     _launch(dev, lib().kda_ssm_decode, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
             _ptr(dt_bias), _ptr(state_pool), _ptr(state_indices), _ptr(y))
     return y
@@ -787,7 +788,7 @@ def ssm_decode_multi(x, dt, A_log, B, C, cu_seqlens, state_pool, state_indices, 
     desc.num_slots = state_pool.shape[0]
     desc.cache_steps = 0 if intermediate_states is None else intermediate_states.shape[1]
     desc.update_pool = 1 if update_pool else 0
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = x.new_empty(x.shape)
     _launch(dev, lib().kda_ssm_decode_multi, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
             _ptr(dt_bias), _ptr(cu_seqlens), _ptr(state_pool), _ptr(state_indices),
             _ptr(intermediate_states) if desc.cache_steps else None, _ptr(y))
@@ -815,9 +816,7 @@ def verify_drafts(tokens, target_probs, cu_seqlens, uniform, uniform_next, *, dr
     _whole(uniform_next, "uniform_next", torch.float32, N, ())
     dev = _on_device(target_probs, (tokens, cu_seqlens, uniform, uniform_next, draft_probs))
     desc = VerifyDesc(N, T, V, _DT[target_probs.dtype], pitch, draft_pitch)
-    accepted = torch.empty(N, dtype=torch.int32, device=dev)
-    next_tokens = torch.empty(N, dtype=torch.int32, device=dev)
-    emitted = torch.empty(T, dtype=torch.int32, device=dev)
+    accepted, next_tokens, emitted = tokens.new_empty((N,)), tokens.new_empty((N,)), tokens.new_empty((T,))
     nbytes = lib().kda_verify_drafts_workspace_size(ctypes.byref(desc))
     ws = _scratch(nbytes, dev)
     _launch(dev, lib().kda_verify_drafts, ctypes.byref(desc), _ptr(tokens), _ptr(target_probs), _ptr(draft_probs), _ptr(cu_seqlens),

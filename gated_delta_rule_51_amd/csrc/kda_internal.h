@@ -90,7 +90,7 @@ struct SsmArgs {
     long x_stride, dt_stride, b_stride, c_stride, z_stride;
 };
 hipError_t launch_ssm_decode(const SsmArgs &a, hipStream_t stream);
-hipError_t launch_ssm_run(const SsmArgs &a, hipStream_t stream);
+hipError_t launch_ssm_multi(const SsmArgs &a, hipStream_t stream);
 hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t stream);
 size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int groups, int p, int s);
 

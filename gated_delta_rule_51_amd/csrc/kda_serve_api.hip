@@ -316,7 +316,7 @@ kda_status kda_ssm_decode_multi(const kda_ssm_desc *d, const void *x, const void
     a.cache = cache;
     a.cache_steps = d->cache_steps;
     a.cache_pitch = d->cache_pitch;
-    return hip_status(launch_ssm_run(a, static_cast<hipStream_t>(stream)));
+    return hip_status(launch_ssm_multi(a, static_cast<hipStream_t>(stream)));
 }
 
 size_t kda_verify_drafts_workspace_size(const kda_verify_desc *d) {
