@@ -87,13 +87,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // take the slots floor(cu[n] / R) + n onwards: at least ceil(L / R) of them lie
 // before the next sequence's first (one where L is 0), so cu_seqlens alone
 // tells what a slot stands for, and floor(T / R) + N slots hold every tile.
-// The whole wave searches, 64 ways a step.
-__device__ __forceinline__ int slot_sequence(const int32_t *cu, int num_seqs, int slot, int R) {
+// With FIRST 0 the tiles after each sequence's first take the slots
+// floor(cu[n] / R) onwards, floor(T / R) in all.  The whole wave searches, 64
+// ways a step.
+template <int FIRST = 1> __device__ __forceinline__ int slot_sequence(const int32_t *cu, int num_seqs, int slot, int R) {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = num_seqs;
     while (n > 1) {
         const int step = (n + 63) / 64, i = lane * step;
-        const unsigned long long m = __ballot(i < n && cu[lo + min(i, n - 1)] / R + lo + i <= slot);
+        const unsigned long long m = __ballot(i < n && cu[lo + min(i, n - 1)] / R + FIRST * (lo + i) <= slot);
         const int k = (63 - __builtin_clzll(m | 1)) * step;
         lo += k;
         n = min(step, n - k);

@@ -20,7 +20,8 @@ template <typename T> __device__ __forceinline__ T uniform(T x) {
 
 struct Segments {
     int len;        // tokens, a multiple of 64
-    int slots;      // floor(T / len) + N
+    int after;      // floor(T / len): at least the segments after the sequences' first
+    int slots;      // after + N places of states
     bool later;     // the last launch
     float *states;  // [slots, H, P, S]: after the segment; before the next one once carried
     float *decays;  // [slots, H]
@@ -33,26 +34,30 @@ struct Place {
     int g, first, last;     // group, first head, one past the group's last head
     long row;               // state row (pool slot or sequence)
     bool skip;              // nothing to do in this launch
+    bool whole;             // forms y, not the state alone
 
-    // whole: the launches that form y, else the one for the states in between
-    __device__ __forceinline__ Place(const SsmArgs &a, const Segments &sg, int hw, bool whole) {
+    __device__ __forceinline__ Place(const SsmArgs &a, const Segments &sg, int hw) {
         const int rep = a.heads / a.groups, blocks = (rep + hw - 1) / hw;
-        sl = (int)blockIdx.x / (a.groups * blocks);
-        const int rest = (int)blockIdx.x % (a.groups * blocks);
+        const int unit = (int)blockIdx.x / (a.groups * blocks), rest = (int)blockIdx.x % (a.groups * blocks);
         g = rest / blocks;
         first = g * rep + rest % blocks * hw;
         last = (g + 1) * rep;
-        const bool single = sg.slots == a.num_seqs;   // every sequence is one segment
-        seq = __builtin_amdgcn_readfirstlane(single ? sl : slot_sequence(a.cu_seqlens, a.num_seqs, sl, sg.len));
+        // The first launch starts with every sequence's first segment, the
+        // longer work; the other units are the segments after the first.
+        const bool head = !sg.later && unit < a.num_seqs;
+        const int after = sg.later ? unit : unit - a.num_seqs;
+        seq = __builtin_amdgcn_readfirstlane(head ? unit : slot_sequence<0>(a.cu_seqlens, a.num_seqs, after, sg.len));
         const int begin = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq]);
         const int all = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq + 1]) - begin;
-        local = single ? 0 : sl - (begin / sg.len + seq);
-        segs = max(1, (all + sg.len - 1) / sg.len);
+        local = head ? 0 : after - begin / sg.len + 1;
+        sl = begin / sg.len + seq + local;
+        segs = all > 0 ? (all - 1) / sg.len + 1 : 1;
         t0 = begin + local * sg.len;
         len = min(sg.len, all - local * sg.len);
         row = seq;
-        skip = local >= segs || (whole ? sg.later != (local > 0) : local == 0 || local == segs - 1) ||
-               (len <= 0 && (a.indices || !a.state_out));
+        whole = sg.later || head;
+        skip = !head && (local >= segs || (!sg.later && local == segs - 1));
+        skip = skip || (len <= 0 && (a.indices || !a.state_out));
         if (!skip && a.indices) {
             row = a.indices[seq];
             if (row < 0) row = a.num_slots - 1;
@@ -94,6 +99,8 @@ __device__ __forceinline__ void m_part(const f32x16 &cb, const float *gate, int 
 }
 
 int ssm_head_workgroups(const SsmArgs &a);   // workgroups of a segment
-hipError_t launch_ssm_chunk_f32(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s);
+// Units of a launch: the sequences' first segments, and those after them.
+inline int ssm_units(const SsmArgs &a, const Segments &sg) { return (sg.later ? 0 : a.num_seqs) + sg.after; }
+hipError_t launch_ssm_chunk_f32(const SsmArgs &a, const Segments &sg, hipStream_t s);
 
 }  // namespace kda

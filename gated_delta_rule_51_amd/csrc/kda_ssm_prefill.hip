@@ -29,11 +29,12 @@
 //
 // Segments.  A chain of chunks is latency bound, and few long sequences leave
 // the chip idle, so sequences are cut into segments.  The first launch runs
-// every sequence's first segment whole, the second the states alone of those
-// between the first and the last, from zero; a third carries the states across
-// them (state = decay of the segment x the state before it + its own); the last
-// runs the other segments whole, each from the state before it.  Sequences of
-// one or two segments thus do no work twice.
+// every sequence's first segment whole and the states alone of those between
+// the first and the last, from zero; a second carries the states across them
+// (state = decay of the segment x the state before it + its own); the last runs
+// the other segments whole, each from the state before it.  Sequences of one or
+// two segments thus do no work twice.
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_ssm_chunk.h"
@@ -99,14 +100,13 @@ template <int PPR> __device__ __forceinline__ int tile_at(int row, int piece) {
     return row * PPR * 16 + ((piece ^ swizzle<PPR>(row & 15)) << 4);   // repeats every 16 rows
 }
 
-template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmArgs a, Segments sg) {
+// A workgroup's segment; without Y its state alone.
+template <int P, int S, typename ST, bool Y>
+__device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg, const Place &at, unsigned char *lds) {
     using C = Chunk<P, S>;
-    extern __shared__ __align__(16) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int hs = wave / C::WPH, pc = wave % C::WPH;   // head of the workgroup, 32-column block of the head
 
-    const Place at(a, sg, C::HW, Y);
-    if (at.skip) return;
     const int g = at.g, first = at.first, h = first + hs, t0 = at.t0, len = at.len;
     const bool active = h < at.last;
 
@@ -513,13 +513,22 @@ template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 2
         }
 }
 
+template <int P, int S, typename ST> __global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmArgs a, Segments sg) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    const Place at(a, sg, Chunk<P, S>::HW);
+    if (at.skip) return;
+    if (at.whole) run_segment<P, S, ST, true>(a, sg, at, lds);
+    else run_segment<P, S, ST, false>(a, sg, at, lds);
+}
+
 // states[k] = decays[k] states[k - 1] + states[k] over a sequence's segments
 // between its first and its last.  grid (quads of a state, sequences on y and z)
 __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Segments sg) {
     const int seq = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
     if (seq >= a.num_seqs) return;
     const long one = (long)a.heads * a.p * a.s, at = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
-    const int begin = a.cu_seqlens[seq], segs = (a.cu_seqlens[seq + 1] - begin + sg.len - 1) / sg.len;
+    const int begin = a.cu_seqlens[seq], all = a.cu_seqlens[seq + 1] - begin;
+    const int segs = all > 0 ? (all - 1) / sg.len + 1 : 1;
     if (segs < 3 || at >= one) return;
     const long sl = begin / sg.len + seq;
     const float *dec = sg.decays + sl * a.heads + at / (a.p * a.s);
@@ -532,31 +541,31 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Segments sg) 
     }
 }
 
-template <int P, int S, typename ST> static hipError_t launch_chunk(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+template <int P, int S, typename ST> static hipError_t launch_chunk(const SsmArgs &a, const Segments &sg, hipStream_t s) {
     using C = Chunk<P, S>;
     static_assert(C::LDS <= 163840, "LDS");
-    const auto kern = whole ? ssm_chunk_kernel<P, S, ST, true> : ssm_chunk_kernel<P, S, ST, false>;
+    const auto kern = ssm_chunk_kernel<P, S, ST>;
     const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
     if (e != hipSuccess) return e;
-    kern<<<dim3(sg.slots * ssm_head_workgroups(a)), 256, C::LDS, s>>>(a, sg);
+    kern<<<dim3(ssm_units(a, sg) * ssm_head_workgroups(a)), 256, C::LDS, s>>>(a, sg);
     return hipGetLastError();
 }
-template <int P, int S> static hipError_t launch_st(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
-    return a.state_bf16 ? launch_chunk<P, S, bf16>(a, sg, whole, s) : launch_chunk<P, S, float>(a, sg, whole, s);
+template <int P, int S> static hipError_t launch_st(const SsmArgs &a, const Segments &sg, hipStream_t s) {
+    return a.state_bf16 ? launch_chunk<P, S, bf16>(a, sg, s) : launch_chunk<P, S, float>(a, sg, s);
 }
-template <int P> static hipError_t launch_s(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+template <int P> static hipError_t launch_s(const SsmArgs &a, const Segments &sg, hipStream_t s) {
     switch (a.s) {
-    case 32: return launch_st<P, 32>(a, sg, whole, s);
-    case 64: return launch_st<P, 64>(a, sg, whole, s);
-    default: return launch_st<P, 128>(a, sg, whole, s);
+    case 32: return launch_st<P, 32>(a, sg, s);
+    case 64: return launch_st<P, 64>(a, sg, s);
+    default: return launch_st<P, 128>(a, sg, s);
     }
 }
-static hipError_t launch_any(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
-    if (!a.io_bf16) return launch_ssm_chunk_f32(a, sg, whole, s);
+static hipError_t launch_any(const SsmArgs &a, const Segments &sg, hipStream_t s) {
+    if (!a.io_bf16) return launch_ssm_chunk_f32(a, sg, s);
     switch (a.p) {
-    case 32: return launch_s<32>(a, sg, whole, s);
-    case 64: return launch_s<64>(a, sg, whole, s);
-    default: return launch_s<128>(a, sg, whole, s);
+    case 32: return launch_s<32>(a, sg, s);
+    case 64: return launch_s<64>(a, sg, s);
+    default: return launch_s<128>(a, sg, s);
     }
 }
 
@@ -570,13 +579,11 @@ static Segments segments_of(int num_seqs, int total_tokens, int head_workgroups)
     Segments sg{};
     const long len = ((long)total_tokens * head_workgroups / 1024 + 63) / 64 * 64;
     const long least = (long)num_seqs * head_workgroups >= 128 ? 512 : 128;
-    sg.len = (int)(len < least ? least : len);
-    if (sg.len >= total_tokens) {   // every sequence is one segment
-        sg.len = (total_tokens + 64) / 64 * 64;
-        sg.slots = num_seqs;
-    } else {
-        sg.slots = total_tokens / sg.len + num_seqs;
-    }
+    sg.len = (int)std::min(std::max(len, least), (long)INT32_MAX - 63);
+    const bool single = sg.len >= total_tokens;   // every sequence is one segment
+    if (single) sg.len = total_tokens > 0 ? total_tokens : 1;
+    sg.after = single ? 0 : total_tokens / sg.len;
+    sg.slots = sg.after + num_seqs;
     return sg;
 }
 static int head_workgroups(int heads, int groups, int p) {
@@ -588,26 +595,25 @@ int ssm_head_workgroups(const SsmArgs &a) { return head_workgroups(a.heads, a.gr
 size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int groups, int p, int s) {
     if (num_seqs <= 0) return 0;
     const Segments sg = segments_of(num_seqs, total_tokens, head_workgroups(heads, groups, p));
-    if (sg.slots == num_seqs) return 0;
+    if (sg.after == 0) return 0;
     return (size_t)sg.slots * heads * ((size_t)p * s + 1) * sizeof(float);
 }
 
 hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t stream) {
     Segments sg = segments_of(a.num_seqs, a.total_tokens, ssm_head_workgroups(a));
-    if (sg.slots == a.num_seqs) return launch_any(a, sg, true, stream);
+    if (sg.after == 0) return launch_any(a, sg, stream);
     const size_t one = (size_t)a.heads * a.p * a.s;
     sg.states = static_cast<float *>(workspace);
     sg.decays = sg.states + sg.slots * one;
-    hipError_t e = launch_any(a, sg, true, stream);
+    hipError_t e = launch_any(a, sg, stream);
     if (e != hipSuccess) return e;
     if (2L * sg.len < a.total_tokens) {   // a sequence of three segments may be there
-        if ((e = launch_any(a, sg, false, stream)) != hipSuccess) return e;
         ssm_carry_kernel<<<dim3((unsigned)((one / 4 + 255) / 256), decode_grid_y(a.num_seqs), decode_grid_z(a.num_seqs)), 256, 0,
                            stream>>>(a, sg);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     sg.later = true;
-    return launch_any(a, sg, true, stream);
+    return launch_any(a, sg, stream);
 }
 
 }  // namespace kda

@@ -38,14 +38,13 @@ template <int PPR> __device__ __forceinline__ int piece_at(int row, int piece) {
     return row * PPR * 16 + ((piece ^ f) << 4);
 }
 
-template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 1) void ssm_chunk_f32_kernel(SsmArgs a, Segments sg) {
+// A workgroup's segment; without Y its state alone.
+template <int P, int S, typename ST, bool Y>
+__device__ __forceinline__ void run_segment_f32(const SsmArgs &a, const Segments &sg, const Place &at, unsigned char *lds) {
     using C = ChunkF<P, S>;
-    extern __shared__ __align__(16) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int hh = lane >> 5, l32 = lane & 31;
     const int hs = wave / C::WPH, pc = wave % C::WPH;   // head of the workgroup, 32-column block of the head
-    const Place at(a, sg, C::HW, Y);
-    if (at.skip) return;
     const int first = at.first, h = first + hs, t0 = at.t0, len = at.len;
     const bool active = h < at.last;
 
@@ -289,27 +288,35 @@ template <int P, int S, typename ST, bool Y> __global__ __launch_bounds__(256, 1
         }
 }
 
-template <int P, int S, typename ST> static hipError_t launch_t(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+template <int P, int S, typename ST> __global__ __launch_bounds__(256, 1) void ssm_chunk_f32_kernel(SsmArgs a, Segments sg) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    const Place at(a, sg, ChunkF<P, S>::HW);
+    if (at.skip) return;
+    if (at.whole) run_segment_f32<P, S, ST, true>(a, sg, at, lds);
+    else run_segment_f32<P, S, ST, false>(a, sg, at, lds);
+}
+
+template <int P, int S, typename ST> static hipError_t launch_t(const SsmArgs &a, const Segments &sg, hipStream_t s) {
     using C = ChunkF<P, S>;
     static_assert(C::LDS <= 163840, "LDS");
-    const auto kern = whole ? ssm_chunk_f32_kernel<P, S, ST, true> : ssm_chunk_f32_kernel<P, S, ST, false>;
+    const auto kern = ssm_chunk_f32_kernel<P, S, ST>;
     const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
     if (e != hipSuccess) return e;
-    kern<<<dim3(sg.slots * ssm_head_workgroups(a)), 256, C::LDS, s>>>(a, sg);
+    kern<<<dim3(ssm_units(a, sg) * ssm_head_workgroups(a)), 256, C::LDS, s>>>(a, sg);
     return hipGetLastError();
 }
-template <int P> static hipError_t launch_s(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+template <int P> static hipError_t launch_s(const SsmArgs &a, const Segments &sg, hipStream_t s) {
     switch (a.s) {
-    case 32: return a.state_bf16 ? launch_t<P, 32, bf16>(a, sg, whole, s) : launch_t<P, 32, float>(a, sg, whole, s);
-    case 64: return a.state_bf16 ? launch_t<P, 64, bf16>(a, sg, whole, s) : launch_t<P, 64, float>(a, sg, whole, s);
-    default: return a.state_bf16 ? launch_t<P, 128, bf16>(a, sg, whole, s) : launch_t<P, 128, float>(a, sg, whole, s);
+    case 32: return a.state_bf16 ? launch_t<P, 32, bf16>(a, sg, s) : launch_t<P, 32, float>(a, sg, s);
+    case 64: return a.state_bf16 ? launch_t<P, 64, bf16>(a, sg, s) : launch_t<P, 64, float>(a, sg, s);
+    default: return a.state_bf16 ? launch_t<P, 128, bf16>(a, sg, s) : launch_t<P, 128, float>(a, sg, s);
     }
 }
-hipError_t launch_ssm_chunk_f32(const SsmArgs &a, const Segments &sg, bool whole, hipStream_t s) {
+hipError_t launch_ssm_chunk_f32(const SsmArgs &a, const Segments &sg, hipStream_t s) {
     switch (a.p) {
-    case 32: return launch_s<32>(a, sg, whole, s);
-    case 64: return launch_s<64>(a, sg, whole, s);
-    default: return launch_s<128>(a, sg, whole, s);
+    case 32: return launch_s<32>(a, sg, s);
+    case 64: return launch_s<64>(a, sg, s);
+    default: return launch_s<128>(a, sg, s);
     }
 }
 
