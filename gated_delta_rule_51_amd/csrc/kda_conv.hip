@@ -13,9 +13,12 @@
 
 namespace kda {
 
-// Tokens per workgroup row of the prefill: the W - 1 rows before it are read
-// again (3 of 35 at four taps, from the caches).
-constexpr int kConvTile = 32;
+// Tokens per workgroup row of the prefill (the W - 1 rows before it are read
+// again, from the caches) and rows loaded ahead.  30,447 tokens x 6144 channels
+// (bf16, four taps; 0.75 GB), y stored past the caches: 16 tokens by 8 rows
+// 132 us (5.7 TB/s), by 16 134, 8 by 8 135, 32 by 16 136; with ordinary stores
+// 16 by 16 147, 32 by 4 160, 64 by 4 174.
+constexpr int kConvTile = 16, kConvAhead = 8;
 
 long conv_prefill_tiles(int num_seqs, int total_tokens) {
     return num_seqs <= 0 ? 0 : (long)total_tokens / kConvTile + num_seqs;
@@ -34,16 +37,19 @@ template <typename IO, int VEC> __device__ __forceinline__ void load_v(const IO 
         }
     }
 }
-template <typename IO, int VEC> __device__ __forceinline__ void store_v(IO *p, const float (&r)[VEC]) {
+template <typename IO, int VEC, bool NT = false> __device__ __forceinline__ void store_v(IO *p, const float (&r)[VEC]) {
     if constexpr (VEC == 1) {
         io_traits<IO>::store(p, 0, r[0]);
     } else if constexpr (VEC == 4) {
-        *reinterpret_cast<f32x4 *>(p) = f32x4{r[0], r[1], r[2], r[3]};
+        const f32x4 w = {r[0], r[1], r[2], r[3]};
+        if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<f32x4 *>(p));
+        else *reinterpret_cast<f32x4 *>(p) = w;
     } else {
         u32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(r[2 * i], r[2 * i + 1]);
-        *reinterpret_cast<u32x4 *>(p) = w;
+        if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
+        else *reinterpret_cast<u32x4 *>(p) = w;
     }
 }
 
@@ -133,7 +139,7 @@ template <typename IO, int VEC, int W> __global__ __launch_bounds__(256) void co
     load_taps<IO, VEC, W>(a, c, wt, bs);
     IO *y = reinterpret_cast<IO *>(a.y) + (long)begin * D + c;
     const int end = min(local + kConvTile, len);
-    constexpr int U = 4;   // rows loaded ahead
+    constexpr int U = kConvAhead;
     int t = local;
     for (; t + U <= end; t += U) {
         float cur[U][VEC];
@@ -143,7 +149,7 @@ template <typename IO, int VEC, int W> __global__ __launch_bounds__(256) void co
         for (int u = 0; u < U; ++u) {
             float o[VEC];
             conv_out<VEC, W>(win, cur[u], wt, bs, a.silu, o);
-            store_v<IO, VEC>(y + (long)(t + u) * D, o);
+            store_v<IO, VEC, true>(y + (long)(t + u) * D, o);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
 #pragma unroll
@@ -156,7 +162,7 @@ template <typename IO, int VEC, int W> __global__ __launch_bounds__(256) void co
         float cur[VEC], o[VEC];
         load_v<IO, VEC>(x + (long)t * a.x_stride, cur);
         conv_out<VEC, W>(win, cur, wt, bs, a.silu, o);
-        store_v<IO, VEC>(y + (long)t * D, o);
+        store_v<IO, VEC, true>(y + (long)t * D, o);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
 #pragma unroll
