@@ -92,6 +92,7 @@ struct SsmArgs {
 hipError_t launch_ssm_decode(const SsmArgs &a, hipStream_t stream);
 hipError_t launch_ssm_multi(const SsmArgs &a, hipStream_t stream);
 hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t stream);
+long ssm_prefill_grid(int num_seqs, int total_tokens, int heads, int groups, int p);   // workgroups of a launch
 size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int groups, int p, int s);
 
 // Draft verification and commit.

@@ -46,7 +46,7 @@ kda_status check_conv(const kda_conv_desc *d, bool pool) {
     if (!d) return KDA_ERR_NULL;
     if (d->num_seqs < 0 || d->total_tokens < 0 || d->channels <= 0 || d->x_stride < d->channels || (pool && d->num_slots <= 0))
         return KDA_ERR_SHAPE;
-    if (d->width < 2 || d->width > 4 || !dtype_ok(d->io_dtype)) return KDA_ERR_UNSUPPORTED;
+    if (d->width < 2 || d->width > 4 || !dtype_ok(d->io_dtype) || d->channels > (1 << 28)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -89,8 +89,11 @@ struct SsmIn {
     const float *A_log, *D, *dt_bias;
 };
 
-// The checks the three scan calls share, for T tokens; fills `a`.
-kda_status ssm_common(const kda_ssm_desc *d, const SsmIn &in, long T, const void *y, const Range (&more)[5], SsmArgs &a) {
+// The checks the three scan calls share, for T tokens; fills `a`.  more: what
+// else is read or written; the states and the cache that are written overlap
+// no input, y overlaps nothing.
+kda_status ssm_common(const kda_ssm_desc *d, const SsmIn &in, long T, const void *y, const Range (&more)[5], const Range &states,
+                      const Range &cache, SsmArgs &a) {
     if (T > 0 && (!in.x || !in.dt || !in.A_log || !in.B || !in.C || !y)) return KDA_ERR_NULL;
     const long hp = (long)d->heads * d->head_dim, gs = (long)d->groups * d->state_dim;
     if (in.z && d->z_stride < hp) return KDA_ERR_SHAPE;
@@ -106,7 +109,7 @@ kda_status ssm_common(const kda_ssm_desc *d, const SsmIn &in, long T, const void
                          {in.B, rows_bytes(T, d->b_stride, gs, isz)}, {in.C, rows_bytes(T, d->c_stride, gs, isz)},
                          {in.z, in.z ? rows_bytes(T, d->z_stride, hp, isz) : 0}, {in.A_log, (size_t)d->heads * 4},
                          {in.D, (size_t)d->heads * 4}, {in.dt_bias, (size_t)d->heads * 4}};
-    if (hits(out, ins) || hits(out, more)) return KDA_ERR_ALIAS;
+    if (hits(out, ins) || hits(out, more) || hits(states, ins) || hits(cache, ins)) return KDA_ERR_ALIAS;
     a = SsmArgs{};
     a.x = in.x; a.dt = in.dt; a.B = in.B; a.C = in.C; a.z = in.z;
     a.A_log = in.A_log; a.D = in.D; a.dt_bias = in.dt_bias;
@@ -155,7 +158,9 @@ kda_status kda_conv_prefill(const kda_conv_desc *d, const void *x, const void *w
     const Range ins[] = {{x, rows_bytes(T, d->x_stride, D, isz)}, {weight, D * d->width * isz}, {bias, D * isz},
                          {cu_seqlens, (size_t)(N + 1) * 4}, {state_indices, (size_t)N * 4}};
     const Range before{state, conv_states(d, pool ? d->num_slots : N)};
-    if (hits(out, ins) || overlap(y, out.n, state, before.n) || hits(last, ins) || overlap(last.p, last.n, y, out.n)) return KDA_ERR_ALIAS;
+    const Range written = !pool ? last : d->update_pool ? before : Range{};
+    if (hits(out, ins) || overlap(y, out.n, state, before.n) || hits(written, ins) || overlap(last.p, last.n, y, out.n))
+        return KDA_ERR_ALIAS;
     if (last.p && last.p != state && overlap(last.p, last.n, state, before.n)) return KDA_ERR_ALIAS;
     if (N == 0 || (T == 0 && (pool || !final_state))) return KDA_OK;
     const kda_status gs = grid_ok((d->channels + 255L) / 256, conv_prefill_tiles(d->num_seqs, d->total_tokens));
@@ -236,21 +241,16 @@ kda_status kda_ssm_prefill(const kda_ssm_desc *d, const void *x, const void *dt,
     const Range before{state, ssm_states(d, pool ? d->num_slots : N)}, last{pool ? nullptr : final_state, ssm_states(d, N)};
     const Range more[5] = {before, last, {cu_seqlens, (size_t)(N + 1) * 4}, {state_indices, (size_t)N * 4}, {workspace, need}};
     SsmArgs a;
-    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, T, y, more, a);
+    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, T, y, more, pool ? before : last, {}, a);
     if (st != KDA_OK) return st;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
-    if (last.p) {
-        const size_t isz = io_size(d->io_dtype);
-        const long hp = (long)d->heads * d->head_dim, gs = (long)d->groups * d->state_dim;
-        const Range ins[] = {{x, rows_bytes(T, d->x_stride, hp, isz)}, {dt, rows_bytes(T, d->dt_stride, d->heads, isz)},
-                             {B, rows_bytes(T, d->b_stride, gs, isz)}, {C, rows_bytes(T, d->c_stride, gs, isz)},
-                             {z, z ? rows_bytes(T, d->z_stride, hp, isz) : 0}, {A_log, (size_t)d->heads * 4},
-                             {D, (size_t)d->heads * 4}, {dt_bias, (size_t)d->heads * 4}, {cu_seqlens, (size_t)(N + 1) * 4},
-                             {workspace, need}};
-        if (hits(last, ins) || (last.p != state && overlap(last.p, last.n, state, before.n))) return KDA_ERR_ALIAS;
-    }
+    const Range written = pool ? before : last;
+    if (overlap(written.p, written.n, cu_seqlens, more[2].n) || overlap(written.p, written.n, state_indices, more[3].n) ||
+        overlap(written.p, written.n, workspace, need) ||
+        (last.p && last.p != state && overlap(last.p, last.n, state, before.n)))
+        return KDA_ERR_ALIAS;
     if (N == 0 || (T == 0 && (pool || !final_state))) return KDA_OK;
-    st = grid_ok((long)d->heads * (d->head_dim / 32) * 64, N);
+    st = grid_ok(ssm_prefill_grid(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim), N);
     if (st != KDA_OK) return st;
     a.cu_seqlens = cu_seqlens;
     a.state_in = state;
@@ -269,8 +269,9 @@ kda_status kda_ssm_decode(const kda_ssm_desc *d, const void *x, const void *dt, 
     if (!state_pool || !state_indices) return KDA_ERR_NULL;
     const Range more[5] = {{state_pool, ssm_states(d, d->num_slots)}, {state_indices, (size_t)n * 4}, {}, {}, {}};
     SsmArgs a;
-    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, n, y, more, a);
+    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, n, y, more, more[0], {}, a);
     if (st != KDA_OK) return st;
+    if (overlap(state_pool, more[0].n, state_indices, more[1].n)) return KDA_ERR_ALIAS;
     st = grid_ok((long)d->heads * (d->head_dim / 32), n);
     if (st != KDA_OK) return st;
     a.state_in = state_pool;
@@ -294,18 +295,11 @@ kda_status kda_ssm_decode_multi(const kda_ssm_desc *d, const void *x, const void
     const Range more[5] = {{state_pool, ssm_states(d, d->num_slots)}, {state_indices, (size_t)N * 4},
                            {cu_seqlens, (size_t)(N + 1) * 4}, kept, {}};
     SsmArgs a;
-    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, T, y, more, a);
+    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, T, y, more, d->update_pool ? more[0] : Range{}, kept, a);
     if (st != KDA_OK) return st;
-    if (cache) {
-        const size_t isz = io_size(d->io_dtype);
-        const long hp = (long)d->heads * d->head_dim, gs = (long)d->groups * d->state_dim;
-        const Range ins[] = {{x, rows_bytes(T, d->x_stride, hp, isz)}, {dt, rows_bytes(T, d->dt_stride, d->heads, isz)},
-                             {B, rows_bytes(T, d->b_stride, gs, isz)}, {C, rows_bytes(T, d->c_stride, gs, isz)},
-                             {z, z ? rows_bytes(T, d->z_stride, hp, isz) : 0}, {A_log, (size_t)d->heads * 4},
-                             {D, (size_t)d->heads * 4}, {dt_bias, (size_t)d->heads * 4}, {cu_seqlens, (size_t)(N + 1) * 4},
-                             {state_indices, (size_t)N * 4}, more[0]};
-        if (hits(kept, ins)) return KDA_ERR_ALIAS;
-    }
+    for (int i = 0; i < 3; ++i)
+        if (overlap(kept.p, kept.n, more[i].p, more[i].n) || (i > 0 && d->update_pool && overlap(state_pool, more[0].n, more[i].p, more[i].n)))
+            return KDA_ERR_ALIAS;
     if (T == 0) return KDA_OK;
     st = grid_ok((long)d->heads * (d->head_dim / 32), N);
     if (st != KDA_OK) return st;

@@ -21,15 +21,15 @@ template <typename T> __device__ __forceinline__ T uniform(T x) {
 struct Segments {
     int len;        // tokens, a multiple of 64
     int after;      // floor(T / len): at least the segments after the sequences' first
-    int slots;      // after + N places of states
     bool later;     // the last launch
-    float *states;  // [slots, H, P, S]: after the segment; before the next one once carried
-    float *decays;  // [slots, H]
+    // Segment k of sequence n, but for its last, has the place floor(cu[n] / len) + k.
+    float *states;  // [after, H, P, S]: after the segment; before the next one once carried
+    float *decays;  // [after, H]
 };
 
 // The segment and heads of a workgroup of HW heads (of one group).
 struct Place {
-    int sl, seq, t0, len;   // slot of the segment, sequence, first token, tokens
+    int place, seq, t0, len;   // the segment's place, sequence, first token, tokens
     int local, segs;        // number of the segment, segments of the sequence
     int g, first, last;     // group, first head, one past the group's last head
     long row;               // state row (pool slot or sequence)
@@ -50,7 +50,7 @@ struct Place {
         const int begin = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq]);
         const int all = __builtin_amdgcn_readfirstlane(a.cu_seqlens[seq + 1]) - begin;
         local = head ? 0 : after - begin / sg.len + 1;
-        sl = begin / sg.len + seq + local;
+        place = begin / sg.len + local;
         segs = all > 0 ? (all - 1) / sg.len + 1 : 1;
         t0 = begin + local * sg.len;
         len = min(sg.len, all - local * sg.len);

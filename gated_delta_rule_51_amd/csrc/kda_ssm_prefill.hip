@@ -124,7 +124,7 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
         for (int u = 0; u < 2; ++u) {
             f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
             if (sg.later) {
-                const float *p = sg.states + (at.sl - 1) * one + in_head + 32 * nt + 16 * u;
+                const float *p = sg.states + (at.place - 1) * one + in_head + 32 * nt + 16 * u;
                 x = load4(p);
                 y = load4(p + 4);
             } else if (a.state_in && at.local == 0) {
@@ -485,7 +485,7 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
 
     const bool last = at.local == at.segs - 1;   // else the state goes to the segment's place
     if (!active || (last ? !a.state_out : sg.later)) return;
-    if (!last && gates && lane == 0) sg.decays[(long)at.sl * a.heads + h] = __builtin_amdgcn_exp2f((float)through);
+    if (!last && gates && lane == 0) sg.decays[(long)at.place * a.heads + h] = __builtin_amdgcn_exp2f((float)through);
     int again = lane;   // the offsets formed anew, not kept through the loop
     asm volatile("" : "+v"(again));
     const long out_head = in_heads(again);
@@ -497,7 +497,7 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e / 4][e % 4] = st[nt][8 * u + e];
             if (!last) {
-                float *p = sg.states + at.sl * one + out_head + 32 * nt + 16 * u;
+                float *p = sg.states + at.place * one + out_head + 32 * nt + 16 * u;
                 *reinterpret_cast<f32x4 *>(p) = x[0];
                 *reinterpret_cast<f32x4 *>(p + 4) = x[1];
                 continue;
@@ -530,9 +530,9 @@ __global__ __launch_bounds__(256) void ssm_carry_kernel(SsmArgs a, Segments sg) 
     const int begin = a.cu_seqlens[seq], all = a.cu_seqlens[seq + 1] - begin;
     const int segs = all > 0 ? (all - 1) / sg.len + 1 : 1;
     if (segs < 3 || at >= one) return;
-    const long sl = begin / sg.len + seq;
-    const float *dec = sg.decays + sl * a.heads + at / (a.p * a.s);
-    float *p = sg.states + sl * one + at;
+    const long place = begin / sg.len;
+    const float *dec = sg.decays + place * a.heads + at / (a.p * a.s);
+    float *p = sg.states + place * one + at;
     f32x4 s = load4(p);
     for (int k = 1; k < segs - 1; ++k) {
         const f32x4 x = load4(p + k * one);
@@ -583,7 +583,6 @@ static Segments segments_of(int num_seqs, int total_tokens, int head_workgroups)
     const bool single = sg.len >= total_tokens;   // every sequence is one segment
     if (single) sg.len = total_tokens > 0 ? total_tokens : 1;
     sg.after = single ? 0 : total_tokens / sg.len;
-    sg.slots = sg.after + num_seqs;
     return sg;
 }
 static int head_workgroups(int heads, int groups, int p) {
@@ -591,12 +590,16 @@ static int head_workgroups(int heads, int groups, int p) {
     return groups * ((rep + hw - 1) / hw);
 }
 int ssm_head_workgroups(const SsmArgs &a) { return head_workgroups(a.heads, a.groups, a.p); }
+long ssm_prefill_grid(int num_seqs, int total_tokens, int heads, int groups, int p) {
+    const int w = head_workgroups(heads, groups, p);
+    return ((long)num_seqs + segments_of(num_seqs, total_tokens, w).after) * w;
+}
 
 size_t ssm_prefill_workspace_bytes(int num_seqs, int total_tokens, int heads, int groups, int p, int s) {
     if (num_seqs <= 0) return 0;
     const Segments sg = segments_of(num_seqs, total_tokens, head_workgroups(heads, groups, p));
     if (sg.after == 0) return 0;
-    return (size_t)sg.slots * heads * ((size_t)p * s + 1) * sizeof(float);
+    return (size_t)sg.after * heads * ((size_t)p * s + 1) * sizeof(float);
 }
 
 hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t stream) {
@@ -604,7 +607,7 @@ hipError_t launch_ssm_prefill(const SsmArgs &a, void *workspace, hipStream_t str
     if (sg.after == 0) return launch_any(a, sg, stream);
     const size_t one = (size_t)a.heads * a.p * a.s;
     sg.states = static_cast<float *>(workspace);
-    sg.decays = sg.states + sg.slots * one;
+    sg.decays = sg.states + sg.after * one;
     hipError_t e = launch_any(a, sg, stream);
     if (e != hipSuccess) return e;
     if (2L * sg.len < a.total_tokens) {   // a sequence of three segments may be there

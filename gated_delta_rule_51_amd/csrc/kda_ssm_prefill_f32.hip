@@ -58,7 +58,7 @@ __device__ __forceinline__ void run_segment_f32(const SsmArgs &a, const Segments
         for (int q = 0; q < 4; ++q) {
             f32x4 x = {0.f, 0.f, 0.f, 0.f};
             const long o = in_head + 32 * nt + 8 * q;
-            if (sg.later) x = load4(sg.states + (at.sl - 1) * one + o);
+            if (sg.later) x = load4(sg.states + (at.place - 1) * one + o);
             else if (a.state_in && at.local == 0) x = load4(reinterpret_cast<const ST *>(a.state_in) + at.row * one + o);
 #pragma unroll
             for (int b = 0; b < 4; ++b) st[nt][4 * q + b] = x[b];
@@ -273,7 +273,7 @@ __device__ __forceinline__ void run_segment_f32(const SsmArgs &a, const Segments
 
     const bool last = at.local == at.segs - 1;   // else the state goes to the segment's place
     if (!active || (last ? !a.state_out : sg.later)) return;
-    if (!last && gates && lane == 0) sg.decays[(long)at.sl * a.heads + h] = __builtin_amdgcn_exp2f((float)through);
+    if (!last && gates && lane == 0) sg.decays[(long)at.place * a.heads + h] = __builtin_amdgcn_exp2f((float)through);
 #pragma unroll
     for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
@@ -282,7 +282,7 @@ __device__ __forceinline__ void run_segment_f32(const SsmArgs &a, const Segments
 #pragma unroll
             for (int b = 0; b < 4; ++b) x[b] = st[nt][4 * q + b];
             const long o = in_head + 32 * nt + 8 * q;
-            if (!last) *reinterpret_cast<f32x4 *>(sg.states + at.sl * one + o) = x;
+            if (!last) *reinterpret_cast<f32x4 *>(sg.states + at.place * one + o) = x;
             else if constexpr (sizeof(ST) == 4) *reinterpret_cast<f32x4 *>(reinterpret_cast<ST *>(a.state_out) + at.row * one + o) = x;
             else *reinterpret_cast<u32x2 *>(reinterpret_cast<ST *>(a.state_out) + at.row * one + o) = u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
         }

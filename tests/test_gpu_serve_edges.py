@@ -1,0 +1,235 @@
+"""Convolution, scan, verification and commit where calls differ from the plain
+ones: rows behind the last sequence, sequences of several segments, graphs
+replayed over other lengths, pools beyond 4 GiB, one index twice in read-only
+calls, calls on two streams, and random shapes."""
+import ctypes
+import random
+
+import pytest
+import torch
+
+import serve_ref as R
+from test_gpu_ssm import Layer, offsets, states
+
+pytestmark = pytest.mark.gpu
+F32, BF, I32 = torch.float32, torch.bfloat16, torch.int32
+DTYPES = {"bf16": BF, "f32": F32}
+
+
+@pytest.fixture(scope="module")
+def K():
+    import gated_delta_rule_51_amd as kda
+    kda.lib()
+    return kda
+
+
+def scan_into(K, m, cu, first, y, n):
+    """kda_ssm_prefill on a caller's y: dense, from first; returns the states."""
+    x, dt, A, B, C = m.args
+    d = K._ssm_desc(x, dt, A, B, C, m.kw.get("D"), m.kw.get("z"), m.kw.get("dt_bias"), n, first.dtype)
+    last = torch.empty_like(first)
+    nbytes = K.lib().kda_ssm_prefill_workspace_size(ctypes.byref(d))
+    ws = torch.full((max(nbytes, 16),), 255, dtype=torch.uint8, device="cuda")   # NaN wherever it is read before it is written
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    K._check(K.lib().kda_ssm_prefill(ctypes.byref(d), p(x), p(dt), p(A), p(B), p(C), p(m.kw.get("D")), p(m.kw.get("z")),
+                                     p(m.kw.get("dt_bias")), p(cu), p(first), None, p(last), p(y), p(ws), nbytes,
+                                     torch.cuda.current_stream().cuda_stream))
+    return last
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,H,P,S,G", [([70, 0, 33], 4, 64, 64, 2), ([900, 5, 0, 700], 2, 128, 32, 1), ([1, 1], 3, 32, 128, 3)])
+def test_rows_behind(K, io, lens, H, P, S, G):
+    """Rows behind the last sequence hold NaN: nothing of them is read, and
+    their outputs stay as they were (a batch padded to a captured size)."""
+    dt, T, pad = DTYPES[io], sum(lens), 130
+    m = Layer(5, T + pad, H, P, S, G, dt)
+    for t in (*m.args[:2], *m.args[3:], m.kw["z"]):
+        t[T:] = float("nan")
+    first = states(m, len(lens), F32)
+    y = torch.full((T + pad, H, P), 7.0, dtype=dt, device="cuda")
+    last = scan_into(K, m, offsets(lens), first.cuda(), y, len(lens))
+    ref = m.ref(lens, first)
+    R.check("y", y[:T], ref["y"][:T], ref["ytol"][:T], dt)
+    R.check("states", last, ref["last"], ref["ltol"], F32)
+    assert bool((y[T:] == 7.0).all())
+    # the convolution and the verify decode
+    g = m.g
+    x = torch.randn(T + pad, 100, generator=g).to(dt)
+    x[T:] = float("nan")
+    w, b = torch.randn(100, 4, generator=g).to(dt), torch.randn(100, generator=g).to(dt)
+    s0 = torch.randn(len(lens), 3, 100, generator=g).to(dt)
+    yc, end = K.conv_prefill(x.cuda(), w.cuda(), b.cuda(), offsets(lens), initial_state=s0.cuda())
+    rc, tol, want = R.conv(x, w, b, lens, s0)
+    R.check("conv", yc[:T], rc, tol, dt)
+    assert (R.f64(end) == want).all()
+    pool = first.cuda()
+    idx = torch.arange(len(lens), dtype=I32, device="cuda")
+    short = [min(n, 9) for n in lens]
+    ref = m.ref(short, first)
+    ym = K.ssm_decode_multi(*m.args, offsets(short), torch.cat([pool, pool[:1]]), idx, **m.kw)
+    R.check("run", ym[:sum(short)], ref["y"][:sum(short)], ref["ytol"][:sum(short)], dt)
+
+
+SEGMENTS = [   # lens, H, P, S, G: at least three segments of 128 or 512 tokens in some
+    ([1500, 3, 0, 700, 129], 2, 64, 64, 1), ([2000], 1, 128, 128, 1), ([128, 256, 257, 640, 1], 5, 32, 128, 1), ([513], 3, 64, 32, 3),
+    ([300] * 40 + [1700], 4, 32, 32, 4),
+]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,H,P,S,G", SEGMENTS, ids=[str(i) for i in range(len(SEGMENTS))])
+def test_segments(K, io, lens, H, P, S, G):
+    dt, T, N = DTYPES[io], sum(lens), len(lens)
+    m = Layer(T, T, H, P, S, G, dt)
+    first = states(m, N, F32)
+    y = torch.empty(T, H, P, dtype=dt, device="cuda")
+    last = scan_into(K, m, offsets(lens), first.cuda(), y, N)
+    ref = m.ref(lens, first)
+    R.check("y", y, ref["y"], ref["ytol"], dt)
+    assert R.check("states", last, ref["last"], ref["ltol"], F32) < 2e-6
+    # in place in a pool, whose rows are read and written by different launches
+    slots = N + 3
+    pool0 = states(m, slots, F32)
+    idx = torch.randperm(slots - 1, generator=m.g)[:N].to(I32)
+    idx[0] = -1
+    at = torch.from_numpy(R.slots_of(idx, slots)).long()
+    pool0[at] = first
+    pool = pool0.cuda()
+    yp, _ = K.ssm_prefill(*m.args, offsets(lens), initial_state=pool, state_indices=idx.cuda(), **m.kw)
+    want = pool0.clone()
+    want[at] = last.cpu()
+    assert torch.equal(yp, y) and torch.equal(pool.cpu(), want)
+
+
+def test_graph_over_other_lengths(K):
+    """One captured step, replayed over other sequences within the captured
+    rows: everything that depends on lengths is found on the GPU."""
+    T, N, H, P, S, G = 1400, 3, 2, 64, 64, 1
+    m = Layer(3, T, H, P, S, G, BF)
+    cu = offsets([T - 2, 1, 1])
+    first = states(m, N, F32).cuda()
+    x = torch.randn(T, 64, generator=m.g).cuda()
+    w = torch.randn(64, 4, generator=m.g).cuda()
+
+    def step():
+        return (*K.ssm_prefill(*m.args, cu, initial_state=first, **m.kw), *K.conv_prefill(x, w, None, cu))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        outs = step()
+    for lens in ([T - 2, 1, 1], [0, 700, 700], [5, 0, 0], [600, 130, 257], [64, 64, 1272]):
+        cu.copy_(offsets(lens))
+        torch.randn(1 << 20, device="cuda").sum()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        want = step()
+        n = sum(lens)
+        for a, b in zip(outs, want):
+            assert torch.equal(a[:n] if a.shape[0] == T else a, b[:n] if b.shape[0] == T else b), lens
+
+
+def test_beyond_4_gib(K):
+    """Pool rows and cached steps past 2^32 bytes give what a small pool gives."""
+    H, P, S, G, N = 32, 128, 128, 2, 3
+    m = Layer(1, 8, H, P, S, G, BF)
+    lens = [3, 4, 1]
+    slots = 2200                                            # 4.6 GB of 2 MiB rows
+    pool = torch.zeros(slots, H, P, S, device="cuda")
+    idx = torch.tensor([2198, 2150, 2101], dtype=I32, device="cuda")
+    some = states(m, N + 1, F32).cuda()
+    pool[idx.long()] = some[:N]
+    small, near = some.clone(), torch.arange(N, dtype=I32, device="cuda")
+    y = K.ssm_decode_multi(*m.args, offsets(lens), pool, idx, **m.kw)
+    assert torch.equal(y, K.ssm_decode_multi(*m.args, offsets(lens), small, near, **m.kw))
+    assert torch.equal(pool[idx.long()], small[:N])
+    cut = [t[:N] if t.dim() > 1 else t for t in m.args]
+    kw = dict(m.kw, z=m.kw["z"][:N])
+    assert torch.equal(K.ssm_decode(*cut, pool, idx, **kw), K.ssm_decode(*cut, small, near, **kw))
+    p1, _ = K.ssm_prefill(*m.args, offsets(lens), initial_state=pool, state_indices=idx, **m.kw)
+    p2, _ = K.ssm_prefill(*m.args, offsets(lens), initial_state=small, state_indices=near, **m.kw)
+    assert torch.equal(p1, p2) and torch.equal(pool[idx.long()], small[:N])
+    cache = pool.view(1, slots, H, P, S).expand(1, slots, H, P, S)        # 2200 steps of one request
+    target = torch.zeros(2, H, P, S, device="cuda")
+    K.commit_states(target, torch.zeros(1, dtype=I32, device="cuda"), cache, torch.tensor([2198], dtype=I32, device="cuda"))
+    assert torch.equal(target[0], pool[2198])
+    del pool, cache
+    D, W = 1 << 20, 4
+    conv = torch.zeros(800, W - 1, D, dtype=BF, device="cuda")            # 5 GB
+    at = torch.tensor([798], dtype=I32, device="cuda")
+    x, w = torch.randn(5, D, device="cuda").to(BF), torch.randn(D, W, device="cuda").to(BF)
+    conv[798] = torch.randn(W - 1, D, device="cuda").to(BF)
+    tiny = torch.stack([conv[798], conv[0]])
+    zero = torch.zeros(1, dtype=I32, device="cuda")
+    a, _ = K.conv_prefill(x, w, None, offsets([5]), initial_state=conv, state_indices=at)
+    b, _ = K.conv_prefill(x, w, None, offsets([5]), initial_state=tiny, state_indices=zero)
+    assert torch.equal(a, b) and torch.equal(conv[798], tiny[0]) and bool((conv[797] == 0).all())
+    assert torch.equal(K.conv_decode(x[:1], w, None, conv, at), K.conv_decode(x[:1], w, None, tiny, zero))
+    assert torch.equal(conv[798], tiny[0])
+
+
+def test_one_index_twice_read_only(K):
+    """Several requests may verify from one pool row, which is only read."""
+    lens = [3, 3, 2]
+    m = Layer(4, 8, 4, 64, 64, 2, BF)
+    for t in (m.args[0], m.args[1], m.args[3], m.args[4], m.kw["z"]):
+        t[3:6] = t[0:3]
+    pool = states(m, 3, F32).cuda()
+    before = pool.clone()
+    cache = torch.zeros(3, 3, 4, 64, 64, device="cuda")
+    idx = torch.ones(3, dtype=I32, device="cuda")
+    y = K.ssm_decode_multi(*m.args, offsets(lens), pool, idx, intermediate_states=cache, update_pool=False, **m.kw)
+    assert torch.equal(y[:3], y[3:6]) and torch.equal(cache[0], cache[1]) and torch.equal(pool, before)
+    conv = torch.randn(4, 3, 40, device="cuda")
+    x, w = torch.randn(8, 40, device="cuda"), torch.randn(40, 4, device="cuda")
+    x[3:6] = x[0:3]
+    keep = conv.clone()
+    yc, _ = K.conv_prefill(x, w, None, offsets(lens), initial_state=conv, state_indices=idx, update_pool=False)
+    assert torch.equal(yc[:3], yc[3:6]) and torch.equal(conv, keep)
+
+
+def test_two_streams(K):
+    """Segmented prompts on two streams at once match the lone calls."""
+    lens = [1500, 40]
+    sets = [Layer(s, sum(lens), 2, 64, 64, 1, BF) for s in (21, 22)]
+    firsts = [states(m, 2, F32).cuda() for m in sets]
+    run = lambda m, f: K.ssm_prefill(*m.args, offsets(lens), initial_state=f, **m.kw)  # noqa: E731
+    want = [run(m, f) for m, f in zip(sets, firsts)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], []
+    for s, m, f in zip(streams, sets, firsts):
+        with torch.cuda.stream(s):
+            got.append([run(m, f) for _ in range(4)])
+    torch.cuda.synchronize()
+    for w, gs in zip(want, got):
+        for y, last in gs:
+            assert torch.equal(y, w[0]) and torch.equal(last, w[1])
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_scans(K, seed):
+    r = random.Random(seed)
+    H = r.choice([1, 2, 3, 5, 6, 8])
+    G = r.choice([g for g in range(1, H + 1) if H % g == 0])
+    P, S = r.choice([32, 64, 128]), r.choice([32, 64, 128])
+    lens = [r.choice([0, 1, 2, 31, 63, 64, 65, r.randint(1, 200)]) for _ in range(r.randint(1, 6))]
+    dt, sd = r.choice([BF, F32]), r.choice([F32, BF])
+    print("seed %d: lens %s H %d P %d S %d G %d %s %s" % (seed, lens, H, P, S, G, dt, sd), flush=True)
+    m = Layer(seed, sum(lens), H, P, S, G, dt, packed=r.random() < 0.5, opts=r.random() < 0.7, decay=r.choice([0.01, 1.0, 5.0]))
+    first = states(m, len(lens), sd)
+    y, last = K.ssm_prefill(*m.args, offsets(lens), initial_state=first.cuda(), **m.kw)
+    ref = m.ref(lens, first)
+    R.check("y", y, ref["y"], ref["ytol"], dt)
+    R.check("states", last, ref["last"], ref["ltol"], sd)
+    slots = len(lens) + 1
+    pool = torch.cat([first, first[:1]]).cuda()
+    idx = torch.arange(len(lens), dtype=I32, device="cuda")
+    y2 = K.ssm_decode_multi(*m.args, offsets(lens), pool, idx, **m.kw)
+    R.check("run", y2, ref["y"], ref["ytol"], dt)
+    R.check("run states", pool[:slots - 1], ref["last"], ref["ltol"], sd)

@@ -70,6 +70,9 @@ def test_conv_refusals(L):
                      (dict(idx=fake(7)), NULL), (dict(idx=fake(7), state=fake(8)), ALIAS),
                      (dict(idx=fake(7), state=fake(8), final=None, y=fake(8, 64)), ALIAS)):
         assert conv(L, d, **kw) == want, kw
+    pool = dict(idx=fake(7), state=fake(8), final=None)
+    assert conv(L, d, x=fake(8, 64), **pool) == ALIAS                                       # the pool is written
+    assert conv(L, conv_desc(channels=(1 << 28) + 1, x_stride=1 << 29)) == UNSUP
     assert conv(L, conv_desc(num_slots=0), idx=fake(7), state=fake(8), final=None) == SHAPE
     assert conv(L, conv_desc(num_seqs=0, total_tokens=0)) == OK
     dec = lambda d, x=fake(1), y=fake(6), pool=fake(8), idx=fake(7): L.kda_conv_decode(  # noqa: E731
@@ -113,6 +116,10 @@ def test_ssm_refusals(L):
                      (dict(idx=fake(13)), NULL), (dict(idx=fake(13), state=fake(14)), ALIAS),
                      (dict(idx=fake(13), state=fake(14), final=None, y=fake(14, 64)), ALIAS)):
         assert ssm(L, d, **kw) == want, kw
+    assert ssm(L, d, idx=fake(13), state=fake(14), final=None, x=fake(14, 1024)) == ALIAS   # the pool is written
+    assert ssm(L, ssm_desc(x_stride=(1 << 22) + 8)) == UNSUP and ssm(L, ssm_desc(z_stride=1 << 23)) == UNSUP
+    many = ssm_desc(num_seqs=1, total_tokens=100000)
+    assert L.kda_ssm_prefill_workspace_size(ctypes.byref(many)) > 0 and ssm(L, many, ws=None) == WS and ssm(L, many, n=64) == WS
     assert ssm(L, ssm_desc(num_seqs=0, total_tokens=0)) == OK
     args = [fake(i) for i in range(1, 9)]
     dec = lambda d, pool=fake(14), idx=fake(13), y=fake(11): L.kda_ssm_decode(ctypes.byref(d), *args, pool, idx, y, None)  # noqa: E731
@@ -122,6 +129,7 @@ def test_ssm_refusals(L):
         ctypes.byref(d), *args, cu, fake(14), fake(13), cache, y, None)
     k = ssm_desc(cache_steps=2, cache_pitch=4)
     assert multi(k, cu=None) == NULL and multi(k, cache=None) == NULL and multi(k, cache=fake(14, 4096)) == ALIAS
+    assert multi(k, cache=fake(4, 512)) == ALIAS and multi(k, cache=fake(13)) == ALIAS and dec(d, pool=fake(13)) == ALIAS
     assert multi(k, cache=fake(15, 4)) == ALIGN and multi(k, y=fake(15)) == ALIAS
     assert multi(ssm_desc(cache_steps=5, cache_pitch=4)) == SHAPE and multi(ssm_desc(total_tokens=0), cache=None) == OK
 
