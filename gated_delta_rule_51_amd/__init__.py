@@ -4,7 +4,8 @@ Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libkda.so``.  PyTorch supplies device memory and the current
 stream.  The library must have been built (``python -m
 gated_delta_rule_51_amd.build``); importing the binding never falls back to
-anything else.
+anything else.  The calls beside the delta rule go through a native module
+(``_binding.so``), as their kernels for one token take a few microseconds.
 
     o, final_state = chunk_prefill(q, k, v, g, beta, cu_seqlens,
                                    initial_state=None, state_indices=None,
@@ -555,21 +556,49 @@ def recurrent_decode_packed_fused_gate(qkv, gate_x, A_log, dt_bias, beta_x, stat
 # ---- short causal convolution, state-space scan, drafts ---------------------
 
 
-# A one-token step takes a few microseconds on the GPU, so what runs around it
-# on the host counts: the checks below test everything in one expression and
-# only then, where it does not hold, find out what to say.
+# A one-token step takes a few microseconds on the GPU, so the checks, outputs
+# and the C call around it are native code.  The functions below hand it their
+# arguments; where something does not fit it declines, and the same checks, one
+# by one in Python, say what.
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+_native_module = None
 
 
-def _launch(dev, fn, *args):
-    """fn(*args, current stream of dev) with dev the current device."""
-    if _get_device() == dev.index:
-        _check(fn(*args, _raw_stream(dev.index) if _raw_stream else _stream(dev)))
+def _native():
+    global _native_module
+    if _native_module is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise KdaError("_binding.so is not built; run `python -m gated_delta_rule_51_amd.build` (%s)" % e)
+        _native_module = _binding
+    return _native_module
+
+
+def _run(name, lead, *args):
+    """The native call `name` on the current stream of lead's device; None
+    where it declines its arguments."""
+    index = lead.get_device()
+    if index < 0:
+        return None
+    fn = getattr(_native_module or _native(), name)
+    if index == torch.cuda.current_device():
+        out = fn(_raw_stream(index), lead, *args)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)))
+        with torch.cuda.device(index):
+            out = fn(_raw_stream(index), lead, *args)
+    if type(out) is int:
+        _check(out)
+    return out
+
+
+def _declined(lead, tensors):
+    """Checks passed one by one, but not in the native call: on other devices,
+    or no plain strided tensors."""
+    _on_device(lead, tensors)
+    raise KdaError("arguments refused: every tensor must be a plain strided one")
 
 
 def _token_rows(t, name, dtype, n, tail):
@@ -611,12 +640,6 @@ def _per_head(t, name, n):
     raise ValueError("%s must have shape [%d], got %s" % (name, n, tuple(t.shape)))
 
 
-def _scratch(nbytes, device):
-    """Workspace of one call, from torch's allocator: held by the graph where
-    the call is captured, so that no two graphs or streams share it."""
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-
-
 def _cu(cu_seqlens):
     _whole(cu_seqlens, "cu_seqlens", torch.int32, 0, ())
     n = cu_seqlens.shape[0] - 1
@@ -628,7 +651,7 @@ def _cu(cu_seqlens):
 def _conv_args(x, weight, bias):
     if x.dim() != 2:
         raise ValueError("x must be [T, D]")
-    dt = _io_dtype(x)
+    _io_dtype(x)
     T, D = x.shape
     if not (weight.dtype is x.dtype and weight.dim() == 2 and weight.shape[0] == D and weight.is_contiguous()):
         _need(weight, "weight", x.dtype, 2)
@@ -636,7 +659,8 @@ def _conv_args(x, weight, bias):
     if bias is not None and not (bias.dtype is x.dtype and bias.shape == (D,) and bias.is_contiguous()):
         _need(bias, "bias", x.dtype, 1)
         raise ValueError("bias must have shape [%d], got %s" % (D, tuple(bias.shape)))
-    return dt, T, D, weight.shape[1], _token_rows(x, "x", x.dtype, T, (D,))
+    _token_rows(x, "x", x.dtype, T, (D,))
+    return D, weight.shape[1]
 
 
 def conv_prefill(x, weight, bias, cu_seqlens, *, initial_state=None, state_indices=None, activation="silu",
@@ -651,58 +675,54 @@ def conv_prefill(x, weight, bias, cu_seqlens, *, initial_state=None, state_indic
     is the pool [slots, W - 1, D], updated in place at state_indices (negative
     -> last slot) unless update_pool is False, and returned.  activation:
     "silu" or None."""
-    dt, T, D, W, stride = _conv_args(x, weight, bias)
     if activation not in ("silu", None):
         raise ValueError("activation must be 'silu' or None")
+    out = _run("conv_prefill", x, weight, bias, cu_seqlens, initial_state, state_indices, activation is not None,
+               bool(output_final_state), bool(update_pool))
+    if out is not None:
+        return out
+    D, W = _conv_args(x, weight, bias)
     N = _cu(cu_seqlens)
     pool = state_indices is not None
     if pool and initial_state is None:
         raise ValueError("pool mode needs the pool as initial_state")
     _whole(initial_state, "state pool" if pool else "initial_state", x.dtype, 1 if pool else N, (W - 1, D))
     _whole(state_indices, "state_indices", torch.int32, N, ())
-    dev = _on_device(x, (weight, bias, cu_seqlens, initial_state, state_indices))
-    desc = ConvDesc(N, T, D, W, dt, 1 if activation else 0, initial_state.shape[0] if pool else 0, 1 if update_pool else 0, stride)
-    y = x.new_empty((T, D))
-    final = initial_state if pool else (torch.empty(N, W - 1, D, dtype=x.dtype, device=dev) if output_final_state else None)
-    _launch(dev, lib().kda_conv_prefill, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(initial_state),
-            _ptr(state_indices), None if pool else _ptr(final), _ptr(y))
-    return y, final
+    _declined(x, (weight, bias, cu_seqlens, initial_state, state_indices))
 
 
 def conv_decode(x, weight, bias, conv_pool, state_indices, *, activation="silu"):
     """One token of B requests through the convolution, in place on the pool
     [slots, W - 1, D].  Returns y [B, D]."""
-    dt, B, D, W, stride = _conv_args(x, weight, bias)
     if activation not in ("silu", None):
         raise ValueError("activation must be 'silu' or None")
+    y = _run("conv_decode", x, weight, bias, conv_pool, state_indices, activation is not None)
+    if y is not None:
+        return y
+    D, W = _conv_args(x, weight, bias)
     _whole(conv_pool, "conv_pool", x.dtype, 1, (W - 1, D))
-    _whole(state_indices, "state_indices", torch.int32, B, ())
-    dev = _on_device(x, (weight, bias, conv_pool, state_indices))
-    desc = ConvDesc(B, B, D, W, dt, 1 if activation else 0, conv_pool.shape[0], 1, stride)
-    y = x.new_empty((B, D))
-    _launch(dev, lib().kda_conv_decode, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(conv_pool), _ptr(state_indices),
-            _ptr(y))
-    return y
+    _whole(state_indices, "state_indices", torch.int32, x.shape[0], ())
+    _declined(x, (weight, bias, conv_pool, state_indices))
 
 
 def conv_commit(x, cu_seqlens, steps, conv_pool, state_indices):
     """After conv_prefill(..., update_pool=False) over drafted tokens: request
     n's pool row becomes the last W - 1 inputs up to its token steps[n] (its
     accepted step; negative, or not below its length: left as it is)."""
+    if _run("conv_commit", x, cu_seqlens, steps, conv_pool, state_indices):
+        return
     if x.dim() != 2:
         raise ValueError("x must be [T, D]")
     T, D = x.shape
-    stride = _token_rows(x, "x", x.dtype, T, (D,))
+    _token_rows(x, "x", x.dtype, T, (D,))
     N = _cu(cu_seqlens)
     if conv_pool.dim() != 3:
         raise ValueError("conv_pool must be [slots, W - 1, D]")
     _whole(conv_pool, "conv_pool", x.dtype, 1, (conv_pool.shape[1], D))
     _whole(state_indices, "state_indices", torch.int32, N, ())
     _whole(steps, "steps", torch.int32, N, ())
-    dev = _on_device(x, (cu_seqlens, steps, conv_pool, state_indices))
-    desc = ConvDesc(N, T, D, conv_pool.shape[1] + 1, _io_dtype(x), 0, conv_pool.shape[0], 1, stride)
-    _launch(dev, lib().kda_conv_commit, ctypes.byref(desc), _ptr(x), _ptr(cu_seqlens), _ptr(steps), _ptr(conv_pool),
-            _ptr(state_indices))
+    _io_dtype(x)
+    _declined(x, (cu_seqlens, steps, conv_pool, state_indices))
 
 
 def _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, num_seqs, state_dtype):
@@ -736,6 +756,12 @@ def ssm_prefill(x, dt, A_log, B, C, cu_seqlens, *, D=None, z=None, dt_bias=None,
     [T, G, S], rows sliced from wider ones or not; A_log, D, dt_bias [H] fp32.
     Returns (y, final_state); dense and pool mode as for chunk_prefill, a state
     being [H, P, S]."""
+    if state_dtype not in (None, torch.float32, torch.bfloat16):
+        raise ValueError("states must be float32 or bfloat16")
+    out = _run("ssm_prefill", x, dt, A_log, B, C, D, z, dt_bias, cu_seqlens, initial_state, state_indices,
+               bool(output_final_state), state_dtype is torch.bfloat16)
+    if out is not None:
+        return out
     N = _cu(cu_seqlens)
     pool = state_indices is not None
     if pool and initial_state is None:
@@ -745,31 +771,20 @@ def ssm_prefill(x, dt, A_log, B, C, cu_seqlens, *, D=None, z=None, dt_bias=None,
     one = (desc.heads, desc.head_dim, desc.state_dim)
     _whole(initial_state, "state pool" if pool else "initial_state", sd, 1 if pool else N, one)
     _whole(state_indices, "state_indices", torch.int32, N, ())
-    dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, initial_state, state_indices))
-    desc.num_slots = initial_state.shape[0] if pool else 0
-    y = x.new_empty(x.shape)
-    final = initial_state if pool else (torch.empty(N, *one, dtype=sd, device=dev) if output_final_state else None)
-    nbytes = lib().kda_ssm_prefill_workspace_size(ctypes.byref(desc))
-    ws = _scratch(nbytes, dev) if nbytes else None
-    _launch(dev, lib().kda_ssm_prefill, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-            _ptr(dt_bias), _ptr(cu_seqlens), _ptr(initial_state), _ptr(state_indices), None if pool else _ptr(final), _ptr(y), _ptr(ws),
-            nbytes)
-    return y, final
+    _declined(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, initial_state, state_indices))
 
 
 def ssm_decode(x, dt, A_log, B, C, state_pool, state_indices, *, D=None, z=None, dt_bias=None):
     """One token of every request through the scan, in place on the pool
     [slots, H, P, S].  Returns y [B, H, P]."""
+    y = _run("ssm_decode", x, dt, A_log, B, C, D, z, dt_bias, state_pool, state_indices)
+    if y is not None:
+        return y
     n = x.shape[0]
     desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, n, state_pool.dtype)
     _whole(state_pool, "state_pool", state_pool.dtype, 1, (desc.heads, desc.head_dim, desc.state_dim))
     _whole(state_indices, "state_indices", torch.int32, n, ())
-    dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, state_pool, state_indices))
-    desc.num_slots = state_pool.shape[0]
-    y = x.new_empty(x.shape)
-    _launch(dev, lib().kda_ssm_decode, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-            _ptr(dt_bias), _ptr(state_pool), _ptr(state_indices), _ptr(y))
-    return y
+    _declined(x, (dt, A_log, B, C, D, z, dt_bias, state_pool, state_indices))
 
 
 def ssm_decode_multi(x, dt, A_log, B, C, cu_seqlens, state_pool, state_indices, *, D=None, z=None, dt_bias=None,
@@ -778,21 +793,17 @@ def ssm_decode_multi(x, dt, A_log, B, C, cu_seqlens, state_pool, state_indices, 
     request n's j-th token goes to intermediate_states[n, j] ([N', steps, H, P,
     S], rows beyond `steps` not kept), the last one to the pool row with
     update_pool.  Returns y [T, H, P]."""
+    y = _run("ssm_decode_multi", x, dt, A_log, B, C, D, z, dt_bias, cu_seqlens, state_pool, state_indices, intermediate_states,
+             bool(update_pool))
+    if y is not None:
+        return y
     N = _cu(cu_seqlens)
     desc = _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, N, state_pool.dtype)
     one = (desc.heads, desc.head_dim, desc.state_dim)
     _whole(state_pool, "state_pool", state_pool.dtype, 1, one)
     _whole(state_indices, "state_indices", torch.int32, N, ())
-    desc.cache_pitch = _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
-    dev = _on_device(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, state_pool, state_indices, intermediate_states))
-    desc.num_slots = state_pool.shape[0]
-    desc.cache_steps = 0 if intermediate_states is None else intermediate_states.shape[1]
-    desc.update_pool = 1 if update_pool else 0
-    y = x.new_empty(x.shape)
-    _launch(dev, lib().kda_ssm_decode_multi, ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A_log), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-            _ptr(dt_bias), _ptr(cu_seqlens), _ptr(state_pool), _ptr(state_indices),
-            _ptr(intermediate_states) if desc.cache_steps else None, _ptr(y))
-    return y
+    _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
+    _declined(x, (dt, A_log, B, C, D, z, dt_bias, cu_seqlens, state_pool, state_indices, intermediate_states))
 
 
 def verify_drafts(tokens, target_probs, cu_seqlens, uniform, uniform_next, *, draft_probs=None):
@@ -804,30 +815,29 @@ def verify_drafts(tokens, target_probs, cu_seqlens, uniform, uniform_next, *, dr
     numbers in [0, 1).  Draft t + 1 stands while uniform[t] q < p.  Returns
     (accepted [N], next_tokens [N], emitted [T]), int32: accepted[n] is the
     step for commit_states and conv_commit (-1: no tokens)."""
+    out = _run("verify_drafts", target_probs, tokens, cu_seqlens, uniform, uniform_next, draft_probs)
+    if out is not None:
+        return out
     _need(tokens, "tokens", torch.int32, 1)
     if target_probs.dim() != 2:
         raise ValueError("target_probs must be [T, V]")
     if target_probs.dtype not in _DT:
         raise ValueError("target_probs must be float32 or bfloat16")
     N, T, V = _cu(cu_seqlens), tokens.shape[0], target_probs.shape[1]
-    pitch = _token_rows(target_probs, "target_probs", target_probs.dtype, T, (V,))
-    draft_pitch = 0 if draft_probs is None else _token_rows(draft_probs, "draft_probs", target_probs.dtype, T, (V,))
+    _token_rows(target_probs, "target_probs", target_probs.dtype, T, (V,))
+    if draft_probs is not None:
+        _token_rows(draft_probs, "draft_probs", target_probs.dtype, T, (V,))
     _whole(uniform, "uniform", torch.float32, T, ())
     _whole(uniform_next, "uniform_next", torch.float32, N, ())
-    dev = _on_device(target_probs, (tokens, cu_seqlens, uniform, uniform_next, draft_probs))
-    desc = VerifyDesc(N, T, V, _DT[target_probs.dtype], pitch, draft_pitch)
-    accepted, next_tokens, emitted = tokens.new_empty((N,)), tokens.new_empty((N,)), tokens.new_empty((T,))
-    nbytes = lib().kda_verify_drafts_workspace_size(ctypes.byref(desc))
-    ws = _scratch(nbytes, dev)
-    _launch(dev, lib().kda_verify_drafts, ctypes.byref(desc), _ptr(tokens), _ptr(target_probs), _ptr(draft_probs), _ptr(cu_seqlens),
-            _ptr(uniform), _ptr(uniform_next), _ptr(accepted), _ptr(next_tokens), _ptr(emitted), _ptr(ws), max(nbytes, 16))
-    return accepted, next_tokens, emitted
+    _declined(target_probs, (tokens, cu_seqlens, uniform, uniform_next, draft_probs))
 
 
 def commit_states(state_pool, state_indices, intermediate_states, steps):
     """state_pool[state_indices[n]] = intermediate_states[n, steps[n]]: the
     accepted step of a verify decode's cache becomes the request's state
     (negative steps, or steps the cache does not hold: left as it is)."""
+    if _run("commit_states", state_pool, state_indices, intermediate_states, steps):
+        return
     if state_pool.dim() != 4 or steps.dim() != 1:
         raise ValueError("state_pool must be [slots, H, V, K] and steps [N]")
     N, one = steps.shape[0], tuple(state_pool.shape[1:])
@@ -836,8 +846,5 @@ def commit_states(state_pool, state_indices, intermediate_states, steps):
     _whole(state_indices, "state_indices", torch.int32, N, ())
     if intermediate_states is None:
         raise ValueError("commit_states needs the step cache")
-    pitch = _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
-    dev = _on_device(state_pool, (state_indices, intermediate_states, steps))
-    desc = CommitDesc(N, state_pool.shape[0], intermediate_states.shape[1], pitch, one[0] * one[1] * one[2] * state_pool.element_size())
-    _launch(dev, lib().kda_commit_states, ctypes.byref(desc), _ptr(state_pool), _ptr(state_indices), _ptr(intermediate_states),
-            _ptr(steps))
+    _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
+    _declined(state_pool, (state_indices, intermediate_states, steps))

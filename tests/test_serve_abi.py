@@ -221,3 +221,19 @@ def test_binding_refusals():
     for call, msg in bad + [(c, "GPU tensors") for c in host]:
         with pytest.raises(ValueError, match=msg):
             call()
+
+
+def test_native_binding(L):
+    """The native module loads, offers every call, and declines host tensors
+    and wrong sizes without a C call."""
+    native = kda._native()
+    x = torch.zeros(2, 4, 32)
+    for name in ("conv_prefill", "conv_decode", "conv_commit", "ssm_prefill", "ssm_decode", "ssm_decode_multi", "verify_drafts",
+                 "commit_states"):
+        assert callable(getattr(native, name)), name
+    none = [None] * 6
+    assert native.ssm_decode(0, x, x[:, :, 0], x[0, :, 0], x, x, None, None, None, x, x) is None
+    assert native.conv_commit(0, x[:, 0], x, x, x, x) is None and native.commit_states(0, x, x, x, x) is None
+    assert native.verify_drafts(0, None, *none[:5]) is None
+    with pytest.raises(TypeError):
+        native.ssm_decode(0, x)
