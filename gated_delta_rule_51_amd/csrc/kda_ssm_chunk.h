@@ -70,10 +70,12 @@ struct Place {
 constexpr int kGateArrays = 5;
 
 // The gates of a chunk, a token a lane: G is the inclusive sum of step x A (A
-// in powers of 2), in fp64.  q points at the lane's place in the arrays.
-// Returns the sum over the chunk.
+// in powers of 2), in fp64.  A token's decay below 2^-1024 counts as that: it
+// is zero either way, and G stays small enough for two floats, whatever the
+// step.  q points at the lane's place in the arrays.  Returns the sum over the
+// chunk.
 __device__ __forceinline__ double write_gates(float *q, float step, double A) {
-    const double G = wave_scan((double)step * A), last = lane_value(G, 63);
+    const double G = wave_scan(fmax((double)step * A, -1024.0)), last = lane_value(G, 63);
     const float gh = (float)G, gl = (float)(G - (double)gh);
     q[0] = gh;
     q[64] = gl;
@@ -92,8 +94,7 @@ __device__ __forceinline__ void m_part(const f32x16 &cb, const float *gate, int 
     const f32x4 gs = *reinterpret_cast<const f32x4 *>(gate + s0), ds = *reinterpret_cast<const f32x4 *>(gate + 128 + s0);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        float x = cb[4 * q + b] * (__builtin_amdgcn_exp2f((gt - gs[b]) + lt) * ds[b]);
-        x = s0 + b == t ? x + Dh : x;
+        const float x = fmaf(cb[4 * q + b], __builtin_amdgcn_exp2f((gt - gs[b]) + lt) * ds[b], s0 + b == t ? Dh : 0.f);
         v[b] = s0 + b <= t ? x : 0.f;
     }
 }

@@ -233,3 +233,24 @@ def test_random_scans(K, seed):
     y2 = K.ssm_decode_multi(*m.args, offsets(lens), pool, idx, **m.kw)
     R.check("run", y2, ref["y"], ref["ytol"], dt)
     R.check("run states", pool[:slots - 1], ref["last"], ref["ltol"], sd)
+
+
+@pytest.mark.parametrize("io", [BF, F32], ids=["bf16", "f32"])
+def test_steps_of_any_size(K, io):
+    """Steps from 0 (softplus underflows) to 1e4 against a rate of 8e36: decays
+    of 0, 1 and between, log-decays beyond fp32, in one chunk and across them."""
+    m = Layer(11, 200, 3, 32, 64, 1, io, opts=False)
+    x, dt, A, B, C = m.args
+    sizes = torch.tensor([-300.0, -100.0, -88.0, -85.0, -84.0, -60.0, 0.0, 3.0, 1e4])
+    pick = torch.randint(0, 9, dt.shape, generator=m.g)
+    pick[70:110] = pick[70:110] % 5      # and a stretch whose states last
+    m.args = (x, sizes[pick].to(io).cuda(), torch.full_like(A, 85.0), B, C)
+    first = states(m, 1, F32)
+    ref = m.ref([200], first)
+    y, last = K.ssm_prefill(*m.args, offsets([200]), initial_state=first.cuda())
+    R.check("y", y, ref["y"], ref["ytol"], io)
+    R.check("states", last, ref["last"], ref["ltol"], F32)
+    pool = first.cuda()
+    y = K.ssm_decode_multi(*m.args, offsets([200]), pool, torch.zeros(1, dtype=I32, device="cuda"))
+    R.check("run", y, ref["y"], ref["ytol"], io)
+    R.check("run states", pool, ref["last"], ref["ltol"], F32)
