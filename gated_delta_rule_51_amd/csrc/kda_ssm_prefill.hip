@@ -50,9 +50,11 @@ __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
 
 // Four rows of a column: of each 16 lanes, lane l reads 8 bytes (4 columns) of
 // row l / 4 and receives column l of the four rows.
-__device__ __forceinline__ u32x2 lds_tr(const unsigned char *p) {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                         (__attribute__((address_space(3))) s16x4 *)(uintptr_t)p));
+__device__ __forceinline__ u32x2 lds_tr(uint32_t at) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)at));
+}
+__device__ __forceinline__ u32x4 lds_row(uint32_t at) {
+    return *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)at;
 }
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
@@ -231,6 +233,16 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
         const int hh = lane >> 5, l32 = lane & 31;
         // transposed reads: row (of 4) and column piece (8 bytes) of this lane within a 32-column block
         const int trow = 4 * hh + ((lane & 15) >> 2), tpiece = 2 * ((lane >> 4) & 1) + (lane & 1), thalf = (lane & 2) << 2;
+        // LDS addresses of the operands: another piece of a row is an exclusive or
+        // away (one instruction; formed from rows and pieces they took five), other
+        // rows and tiles a constant
+        const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+        const uint32_t row_at = lds0 + tile_at<C::PPR>(l32, hh);
+        const uint32_t x_at[2] = {lds0 + tile_at<16>(trow, 4 * wave + tpiece) + thalf, lds0 + tile_at<16>(trow + 8, 4 * wave + tpiece) + thalf};
+        const uint32_t b_at[2] = {lds0 + tile_at<C::PPR>(trow, tpiece) + thalf, lds0 + tile_at<C::PPR>(trow + 8, tpiece) + thalf};
+        const auto operand_row = [&](int part, int rows, int u) {   // rows of 32 of B or C, pieces 2u and 2u + 1
+            return lds_row((row_at ^ (u << 5)) + part + rows * 32 * C::PPR * 16);
+        };
         unsigned char *const mbase = lds + C::OFF_M + hs * C::MBYTES + lane * 16;
         unstage_xb(lane);
         if constexpr (Y && C::WPH == 1) unstage_c(lane);
@@ -251,9 +263,7 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
             for (int i = 0; i < 16; ++i) acc[i] = 0.f;
 #pragma unroll
             for (int u = 0; u < S / 16; ++u) {
-                const u32x4 bo = *reinterpret_cast<const u32x4 *>(lds + C::OFF_B + tile_at<C::PPR>(32 * ss + l32, 2 * u + hh));
-                const u32x4 co = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(32 * tt + l32, 2 * u + hh));
-                acc = mfma(bo, co, acc);
+                acc = mfma(operand_row(C::OFF_B, ss, u), operand_row(C::OFF_C, tt, u), acc);
             }
             return acc;
         };
@@ -295,14 +305,14 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
             u32x4 co[2];   // C's operand of one step ahead
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
-                co[tt] = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(32 * tt + l32, hh));
+                co[tt] = operand_row(C::OFF_C, tt, 0);
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 u32x4 cn[2];
                 if (i + 1 < NS) {
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt)
-                        cn[tt] = *reinterpret_cast<const u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(32 * tt + l32, 2 * (i + 1) + hh));
+                        cn[tt] = operand_row(C::OFF_C, tt, i + 1);
                 }
                 float v[8];
 #pragma unroll
@@ -359,14 +369,12 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
         u32x4 zr[2][2], xo, bo[3], mo[2][2];
         f32x4 w[2];
         auto operand_x = [&](int k) {
-            const u32x2 x0 = lds_tr(lds + tile_at<16>(16 * k + trow, 4 * wave + tpiece) + thalf);
-            const u32x2 x1 = lds_tr(lds + tile_at<16>(16 * k + trow + 8, 4 * wave + tpiece) + thalf);
+            const u32x2 x0 = lds_tr(x_at[0] + k * 16 * 256), x1 = lds_tr(x_at[1] + k * 16 * 256);
             return u32x4{x0[0], x0[1], x1[0], x1[1]};
         };
         auto operand_b = [&](int step) {
-            const int row = 16 * (step / C::NT) + trow, piece = 4 * (step % C::NT) + tpiece;
-            const u32x2 b0 = lds_tr(lds + C::OFF_B + tile_at<C::PPR>(row, piece) + thalf);
-            const u32x2 b1 = lds_tr(lds + C::OFF_B + tile_at<C::PPR>(row + 8, piece) + thalf);
+            const int nt = step % C::NT, part = C::OFF_B + step / C::NT * 16 * C::PPR * 16;
+            const u32x2 b0 = lds_tr((b_at[0] ^ (nt << 6)) + part), b1 = lds_tr((b_at[1] ^ (nt << 6)) + part);
             return u32x4{b0[0], b0[1], b1[0], b1[1]};
         };
         auto operands_m = [&](int k) {
@@ -514,7 +522,7 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
 }
 
 template <int P, int S, typename ST> __global__ __launch_bounds__(256, 2) void ssm_chunk_kernel(SsmArgs a, Segments sg) {
-    extern __shared__ __align__(16) unsigned char lds[];
+    extern __shared__ __align__(1024) unsigned char lds[];   // rows of pieces start on 256 bytes
     const Place at(a, sg, Chunk<P, S>::HW);
     if (at.skip) return;
     if (at.whole) run_segment<P, S, ST, true>(a, sg, at, lds);
