@@ -22,13 +22,18 @@ constexpr int kPart = 4 * 64 * kVec;               // tokens of a part: a multip
 static int part_tokens(int vocab) {
     return (int)((((long)vocab + kVerifyParts - 1) / kVerifyParts + kPart - 1) / kPart * kPart);
 }
-int verify_parts(int, int vocab) { return (int)(((long)vocab + part_tokens(vocab) - 1) / part_tokens(vocab)); }
+int verify_parts(int vocab) { return (int)(((long)vocab + part_tokens(vocab) - 1) / part_tokens(vocab)); }
 
-// Workgroups a row's parts are summed by: one, which then finds the token as
-// well, where the requests fill the chip by themselves, else a wave a part.
-// Measured at V = 65,536 (64 parts), one and eight: see the launch below.
+// Workgroups a row's parts are summed by.  One finds the token as well, in one
+// launch; with more a wave takes a part and a second launch finds the token.
+// One is for rows of 8 waves' parts, and for many requests with rows of up to
+// 32 parts.  Measured with runs of four, one against several (us):
+//     tokens    1 request      128          256         512         1024
+//     32,768    22 / 14     25 / 21     32 / 38     49 / 51     84 / 84
+//     65,536    32 / 14     42 / 33     50 / 51     82 / 81    138 / 135
+//     131,072   54 / 13     72 / 50     87 / 80    134 / 127   218 / 198
 static int verify_groups(int num_seqs, int parts) {
-    return num_seqs >= 256 ? 1 : (parts + kVerifyWaves - 1) / kVerifyWaves;
+    return num_seqs >= 256 && parts <= 32 ? 1 : (parts + kVerifyWaves - 1) / kVerifyWaves;
 }
 
 struct Verdict {
@@ -37,7 +42,7 @@ struct Verdict {
     bool refused;
 };
 
-template <typename PT> __device__ __forceinline__ Verdict judge(const VerifyArgs &a, int n, int lane) {
+template <typename PT> __device__ __forceinline__ Verdict verdict_of(const VerifyArgs &a, int n, int lane) {
     Verdict v;
     v.t0 = a.cu_seqlens[n];
     v.len = a.cu_seqlens[n + 1] - v.t0;
@@ -246,7 +251,7 @@ template <typename PT> __global__ __launch_bounds__(kVerifyThreads) void verify_
     const int n = (int)blockIdx.y + (int)blockIdx.z * (int)gridDim.y;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (n >= a.num_seqs) return;
-    const Verdict v = judge<PT>(a, n, lane);
+    const Verdict v = verdict_of<PT>(a, n, lane);
     if (v.len <= 0) {
         if (blockIdx.x == 0 && threadIdx.x == 0) {
             a.accepted[n] = -1;

@@ -106,7 +106,7 @@ struct VerifyArgs {
     bool bf16;
     long target_stride, draft_stride;
 };
-int verify_parts(int num_seqs, int vocab);
+int verify_parts(int vocab);
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t stream);
 hipError_t launch_commit(const int32_t *indices, const int32_t *steps, const void *cache, void *pool, int num_seqs,
                          int num_slots, int cache_steps, int cache_pitch, long row_bytes, hipStream_t stream);

@@ -315,7 +315,7 @@ kda_status kda_ssm_decode_multi(const kda_ssm_desc *d, const void *x, const void
 
 size_t kda_verify_drafts_workspace_size(const kda_verify_desc *d) {
     if (check_verify(d) != KDA_OK) return 0;
-    return (size_t)d->num_seqs * (1 + 2 * (size_t)verify_parts(d->num_seqs, d->vocab)) * sizeof(double);
+    return (size_t)d->num_seqs * (1 + 2 * (size_t)verify_parts(d->vocab)) * sizeof(double);
 }
 
 kda_status kda_verify_drafts(const kda_verify_desc *d, const int32_t *tokens, const void *target_probs, const void *draft_probs,
@@ -351,7 +351,7 @@ kda_status kda_verify_drafts(const kda_verify_desc *d, const int32_t *tokens, co
     a.accepted = accepted; a.next = next_tokens; a.emitted = emitted;
     a.partial = static_cast<double *>(workspace);
     a.num_seqs = d->num_seqs; a.vocab = d->vocab;
-    a.parts = verify_parts(d->num_seqs, d->vocab);
+    a.parts = verify_parts(d->vocab);
     a.bf16 = d->prob_dtype == KDA_BF16;
     a.target_stride = d->target_stride; a.draft_stride = d->draft_stride;
     return hip_status(launch_verify(a, static_cast<hipStream_t>(stream)));

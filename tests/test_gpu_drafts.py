@@ -98,6 +98,14 @@ def test_borders(K):
     check(K, lens, p, None, tokens, u, r)
 
 
+@pytest.mark.parametrize("V", [20001, 40001])
+def test_many_requests_long_rows(K, V):
+    """Rows summed by one workgroup, and by several with a second launch."""
+    lens = [1, 3, 2, 0, 1] * 52
+    p, q, tokens, u, r = make(V, lens, V, F32)
+    check(K, lens, p, q, tokens, u, r)
+
+
 def test_verify_empty(K):
     z = lambda *s, dtype=F32: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
     acc, nxt, out = K.verify_drafts(z(0, dtype=I32), z(0, 9), offsets([0, 0]).cuda(), z(0), z(2))
