@@ -7,6 +7,11 @@
 // per channel p of the head, the S states contiguous) of state[slot, h]; rows
 // are independent given B, C and the step.  Bound by the state's bytes, read
 // once and written once with 16-byte nontemporal accesses.
+//
+// Measured: one token of 4096 requests x 32 heads x (128 x 128) 3.00 ms
+// (17.3 GB, 5.8 TB/s); of one request 4.2 us, a launch and a row's latency; four
+// tokens of 1024 requests x 32 heads x (64 x 128), every state cached, 1.09 ms
+// (5.4 GB, 5.0 TB/s, four fifths of it writes; at 128 x 128 6.0 TB/s).
 #include "kda_device.h"
 #include "kda_internal.h"
 #include "kda_rows.h"

@@ -439,7 +439,13 @@ typedef struct {
  *   A_log [H], D [H] or NULL, dt_bias [H] or NULL: fp32
  *   state, state_indices, final_state, cu_seqlens: as for kda_chunk_prefill
  *   y  [T, H, P] io dtype, contiguous; must not overlap any input
- * Precision: fp32 throughout.  Not checked: inputs are finite.
+ * Precision: states and sums are fp32, sums of log-decays fp64 (a token's
+ * log-decay, in powers of 2, below -1024 counts as that).  kda_ssm_prefill's
+ * products run on the matrix cores: with fp32 io on fp32 operands; with bf16 io
+ * on bf16 operands, x, B and C as they are and every fp32 factor as the sum of
+ * two bf16 terms for y (2^-17 of the factor, below y's own rounding) and of
+ * three for the states (2^-26).  The other entry points compute in fp32.
+ * Not checked: inputs are finite.
  */
 size_t kda_ssm_prefill_workspace_size(const kda_ssm_desc *desc);
 kda_status kda_ssm_prefill(const kda_ssm_desc *desc, const void *x, const void *dt,
