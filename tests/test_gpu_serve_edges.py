@@ -254,3 +254,47 @@ def test_steps_of_any_size(K, io):
     y = K.ssm_decode_multi(*m.args, offsets([200]), pool, torch.zeros(1, dtype=I32, device="cuda"))
     R.check("run", y, ref["y"], ref["ytol"], io)
     R.check("run states", pool, ref["last"], ref["ltol"], F32)
+
+
+@pytest.mark.parametrize("io", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("S,sd,H,G", [(128, F32, 32, 8), (128, F32, 33, 11), (32, BF, 32, 16), (32, BF, 33, 11), (64, F32, 36, 6)])
+def test_whole_heads(K, io, S, sd, H, G):
+    """Batches whose workgroups take one or two whole heads of 64 rows give the
+    bits of the same requests in small batches, and those the reference's."""
+    P, B, L = 64, 72, [1, 3, 2, 0, 4, 2] * 12
+    m = Layer(S + H, sum(L), H, P, S, G, io)
+    first = states(m, B + 1, sd)
+    idx = torch.randperm(B, generator=m.g).to(I32)
+    cut = lambda t, a, b: None if t is None else t[a:b]  # noqa: E731
+
+    def run(a, b):
+        """Requests a .. b - 1: y, the pool, the step cache."""
+        t0, t1 = sum(L[:a]), sum(L[:b])
+        x, dt, A, Bm, C = m.args
+        kw = dict(m.kw, z=cut(m.kw["z"], t0, t1))
+        pool, cache = first.cuda(), torch.full((b - a, 3, H, P, S), 5.0, dtype=sd, device="cuda")
+        y = K.ssm_decode_multi(x[t0:t1], dt[t0:t1], A, Bm[t0:t1], C[t0:t1], offsets(L[a:b]), pool, idx[a:b].cuda(),
+                               intermediate_states=cache, **kw)
+        return y, pool[idx[a:b].long().cuda()], cache
+
+    whole = run(0, B)
+    few = [run(a, a + 6) for a in range(0, B, 6)]
+    for k in range(3):
+        assert torch.equal(whole[k], torch.cat([f[k] for f in few])), k
+    ref = m.ref(L[:6], first[idx[:6].long()])
+    R.check("y", few[0][0], ref["y"][:sum(L[:6])], ref["ytol"][:sum(L[:6])], io)
+    R.check("states", few[0][1], ref["last"], ref["ltol"], sd)
+
+
+@pytest.mark.parametrize("H,G", [(32, 16), (33, 11)])
+def test_whole_heads_of_one_token(K, H, G):
+    P, S, B = 64, 32, 540
+    m = Layer(H, B, H, P, S, G, BF)
+    first = states(m, B + 1, BF)
+    idx = torch.randperm(B, generator=m.g).to(I32).cuda()
+    x, dt, A, Bm, C = m.args
+    run = lambda p, a, b: K.ssm_decode(x[a:b], dt[a:b], A, Bm[a:b], C[a:b], p, idx[a:b], **dict(m.kw, z=m.kw["z"][a:b]))  # noqa: E731
+    pool, small = first.cuda(), first.cuda()
+    y = run(pool, 0, B)
+    ys = torch.cat([run(small, a, a + 60) for a in range(0, B, 60)])
+    assert torch.equal(y, ys) and torch.equal(pool, small)
