@@ -19,11 +19,13 @@
 // order; its k slots are {4h + b, 8 + 4h + b} of every 16 tokens, and the
 // transposed reads of x and B take their rows in that order.
 //
-// Precision.  x, B and C are bf16 and enter exactly.  What is fp32 enters as a
-// sum of bf16 terms: M and S in two (remainder 2^-17 of the value, far below
-// y's own rounding of 2^-9), dt x exp(.) in three (2^-26), so that the fp32
-// states keep fp32's accuracy, in the whole range of bf16.  The sums G are
-// formed in fp64 and kept as two floats: differences of large sums would
+// Precision.  x, B and C are bf16 and enter exactly.  What is fp32 (M, S and
+// dt x exp(.)) enters as the sum of three bf16 terms, which hold all its 24
+// bits, so y and the states keep fp32's accuracy, also where large parts of a
+// state cancel in S C or of M in M x; two terms (17 bits) lost y there, and
+// elsewhere changed y's last bit four times as often.  They took 349 and 278 us
+// for the two workloads below in a run where three take 390 and 294.  The sums
+// G are formed in fp64 and kept as two floats: differences of large sums would
 // otherwise lose the small decays between neighbours.
 //
 // Segments.  A chain of chunks is latency bound, and few long sequences leave
@@ -34,16 +36,12 @@
 // the other segments whole, each from the state before it.  Sequences of one or
 // two segments thus do no work twice.
 //
-// What bounds it.  At P = S = 128 a wave's chunk takes 100 products of 32
-// cycles and about 1000 vector instructions of 4, two waves a SIMD, most of them
+// What bounds it.  At P = S = 128 a wave's chunk takes 122 products of 32
+// cycles and about 1200 vector instructions of 4, two waves a SIMD, most of them
 // the splitting of fp32 operands, the gating by z and M's exponentials, so the
-// vector units set the pace; the matrix cores are a third to two fifths busy,
-// memory at 2 TB/s.  16 prompts of 512 to 4096 tokens x 32 heads x (128 x 128):
-// 346 us (0.69 GB, 64 GFLOP); one of 32,768 x 32 heads x (64 x 128), gated:
-// 274 us, of which the first launch takes 100 and the carry 23.  Operand
-// addresses formed from rows and pieces, and softplus by the library's log1p and
-// exp, took 361 and 289 us.  A state in one bf16 term, or the weighted x in two,
-// would take fewer instructions, but their error (2^-9, 2^-17) would show.
+// vector units set the pace; memory is at 1.8 TB/s.  16 prompts of 512 to 4096
+// tokens x 32 heads x (128 x 128): 375 to 390 us by the run (0.69 GB, 64 GFLOP);
+// one of 32,768 x 32 heads x (64 x 128), gated: 287 to 294 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -70,20 +68,25 @@ __device__ __forceinline__ u32x4 lds_row(uint32_t at) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// v as bf16 terms: t[0] + t[1] (+ t[2]).
-template <int TERMS> __device__ __forceinline__ void split(const float (&v)[8], u32x4 (&t)[TERMS]) {
+// Two floats as words of three bf16 terms each, t[0] + t[1] + t[2], exactly: a
+// term is cut off after 8 bits, not rounded, so three hold the 24 and the first
+// never passes the value (rounded, one above bf16's largest became infinite).
+constexpr int kTerms = 3;
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[kTerms]) {
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) {
+        t[k] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302);   // both upper halves
+        x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+        y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void split(const float (&v)[8], u32x4 (&t)[kTerms]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float x = v[2 * i], y = v[2 * i + 1];
+        uint32_t w[kTerms];
+        split2(v[2 * i], v[2 * i + 1], w);
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k) {
-            const uint32_t w = pack2(x, y);
-            t[k][i] = w;
-            if (k + 1 < TERMS) {
-                x -= lo_f(w);
-                y -= hi_f(w);
-            }
-        }
+        for (int k = 0; k < kTerms; ++k) t[k][i] = w[k];
     }
 }
 
@@ -93,10 +96,14 @@ template <int P, int S> struct Chunk {
     static constexpr int NT = S / 32;           // 32-wide tiles of the state's columns
     static constexpr int PPR = S / 8;           // 16-byte pieces of a row of B
     static constexpr int PB = PPR / 4;          // pieces of B a thread stages
-    static constexpr int MBYTES = WPH == 1 ? 0 : 3 * 2 * 2 * 1024;   // M of one head
     static constexpr int OFF_B = 64 * 256, OFF_C = OFF_B + 64 * 2 * S, OFF_M = OFF_C + 64 * 2 * S;
-    static constexpr int OFF_G = OFF_M + HW * MBYTES;
     static constexpr int GBYTES = HW * kGateArrays * 256;            // one buffer of gates
+    // M of a head, three tiles: as terms, each formed once, or as floats that every
+    // wave of the head splits, where terms would leave no room for two workgroups
+    static constexpr int TERM_BYTES = 3 * 2 * kTerms * 1024;
+    static constexpr bool MTERMS = WPH > 1 && OFF_M + HW * TERM_BYTES + 2 * GBYTES <= 81920;
+    static constexpr int MBYTES = WPH == 1 ? 0 : MTERMS ? TERM_BYTES : 3 * 4096;
+    static constexpr int OFF_G = OFF_M + HW * MBYTES;
     static constexpr int LDS = OFF_G + 2 * GBYTES;
 };
 
@@ -277,20 +284,18 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
             }
             return acc;
         };
-        auto form_m = [&](int tt, int ss, u32x4(&mt)[2][2]) {
+        auto form_m = [&](int tt, int ss, float(&mt)[2][8]) {
             const f32x16 cb = products(tt, ss);
             const float gt = gate[32 * tt + l32], lt = gate[64 + 32 * tt + l32];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float v[2][4], all[8];
-                m_part(cb, gate, tt, ss, 2 * u, lane, Dh, gt, lt, v[0]);
-                m_part(cb, gate, tt, ss, 2 * u + 1, lane, Dh, gt, lt, v[1]);
+            for (int q = 0; q < 4; ++q) {
+                float v[4];
+                m_part(cb, gate, tt, ss, q, lane, Dh, gt, lt, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) all[e] = v[e / 4][e % 4];
-                split<2>(all, mt[u]);
+                for (int b = 0; b < 4; ++b) mt[q / 2][4 * (q % 2) + b] = v[b];
             }
         };
-        u32x4 m[2][2][2];
+        float m[2][2][8];
         if (gates && more) {
             make_gates(c0 + 64, buf ^ 1, lane);
             fetch_dt(c0 + 128, lane);
@@ -327,10 +332,10 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = st[i / 2][8 * (i % 2) + e];
-                u32x4 s[2];
-                split<2>(v, s);
+                u32x4 s[kTerms];
+                split(v, s);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < kTerms; ++j)
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) y[tt] = mfma(s[j], co[tt], y[tt]);
 #pragma unroll
@@ -340,17 +345,20 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
                     m_part(cb[j], gate, tile > 0, tile > 1, q, lane, Dh, gt[j], lt[j], v4);
 #pragma unroll
                     for (int b = 0; b < 4; ++b) mv[4 * (q % 2) + b] = v4[b];
-                    if (q % 2) {
-                        u32x4 mt[2];
-                        split<2>(mv, mt);
+                    if (C::MTERMS && q % 2) {
+                        u32x4 mt[kTerms];
+                        split(mv, mt);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) *reinterpret_cast<u32x4 *>(mbase + (tile * 4 + q / 2 * 2 + k) * 1024) = mt[k];
+                        for (int k = 0; k < kTerms; ++k)
+                            *reinterpret_cast<u32x4 *>(mbase + ((tile * 2 + q / 2) * kTerms + k) * 1024) = mt[k];
+                    } else if (!C::MTERMS) {
+                        *reinterpret_cast<f32x4 *>(mbase + (tile * 4 + q) * 1024) = f32x4{v4[0], v4[1], v4[2], v4[3]};
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {   // a product, then arithmetic that runs under it
+                for (int j = 0; j < 2 * kTerms; ++j) {   // a product, then arithmetic that runs under it
                     __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x2, TILES == 0 ? 7 : 11, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, TILES == 0 ? 10 : 14, 0);
                 }
                 co[0] = cn[0];
                 co[1] = cn[1];
@@ -376,7 +384,7 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
 
         // y += M x;  S += (weights x) B^T, 16 tokens at a time, B's operands two
         // products ahead, with the next chunk's rows loaded in between
-        u32x4 zr[2][2], xo, bo[3], mo[2][2];
+        u32x4 zr[2][2], xo, bo[3], mo[2][C::MTERMS ? kTerms : 2];
         f32x4 w[2];
         auto operand_x = [&](int k) {
             const u32x2 x0 = lds_tr(x_at[0] + k * 16 * 256), x1 = lds_tr(x_at[1] + k * 16 * 256);
@@ -389,11 +397,12 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
         };
         auto operands_m = [&](int k) {
             if constexpr (Y && C::WPH > 1) {
+                constexpr int each = C::MTERMS ? kTerms : 2;
 #pragma unroll
                 for (int tt = k >> 1; tt < 2; ++tt)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        mo[tt][j] = *reinterpret_cast<const u32x4 *>(mbase + ((tt + (k >> 1)) * 4 + (k & 1) * 2 + j) * 1024);
+                    for (int j = 0; j < each; ++j)
+                        mo[tt][j] = *reinterpret_cast<const u32x4 *>(mbase + (((tt + (k >> 1)) * 2 + (k & 1)) * each + j) * 1024);
             }
         };
         auto weights = [&](int k) {
@@ -401,16 +410,12 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
             w[1] = *reinterpret_cast<const f32x4 *>(gate + 192 + 16 * k + 8 + 4 * hh);
         };
         // words e of the three terms of weight x x
-        u32x4 wx[3];
+        u32x4 wx[kTerms];
         auto weigh = [&](int e) {
-            float p = lo_f(xo[e]) * w[e / 2][2 * e % 4], q = hi_f(xo[e]) * w[e / 2][(2 * e + 1) % 4];
+            uint32_t t[kTerms];
+            split2(lo_f(xo[e]) * w[e / 2][2 * e % 4], hi_f(xo[e]) * w[e / 2][(2 * e + 1) % 4], t);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const uint32_t t = pack2(p, q);
-                wx[j][e] = t;
-                p -= lo_f(t);
-                q -= hi_f(t);
-            }
+            for (int j = 0; j < kTerms; ++j) wx[j][e] = t[j];
         };
         xo = operand_x(0);
         operands_m(0);
@@ -442,10 +447,25 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
                 }
             }
             if constexpr (Y) {
+                u32x4 mt[2][kTerms];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int tt = ss; tt < 2; ++tt) {
+                    if constexpr (C::MTERMS) {
 #pragma unroll
-                    for (int tt = ss; tt < 2; ++tt) y[tt] = mfma(xo, C::WPH == 1 ? m[tt][u][j] : mo[tt][j], y[tt]);
+                        for (int j = 0; j < kTerms; ++j) mt[tt][j] = mo[tt][j];
+                    } else if constexpr (C::WPH == 1) {
+                        split(m[tt][u], mt[tt]);
+                    } else {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(mo[tt][e / 4][e % 4]);
+                        split(v, mt[tt]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kTerms; ++j)
+#pragma unroll
+                    for (int tt = ss; tt < 2; ++tt) y[tt] = mfma(xo, mt[tt][j], y[tt]);
             }
             // The next 16 tokens' weighted x is split between this one's products,
             // and the state decays just before its first.

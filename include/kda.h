@@ -443,8 +443,8 @@ typedef struct {
  * log-decay, in powers of 2, below -1024 counts as that).  kda_ssm_prefill's
  * products run on the matrix cores: with fp32 io on fp32 operands; with bf16 io
  * on bf16 operands, x, B and C as they are and every fp32 factor as the sum of
- * two bf16 terms for y (2^-17 of the factor, below y's own rounding) and of
- * three for the states (2^-26).  The other entry points compute in fp32.
+ * three bf16 terms, which hold all its bits.  The other entry points compute in
+ * fp32.
  * Not checked: inputs are finite.
  */
 size_t kda_ssm_prefill_workspace_size(const kda_ssm_desc *desc);
