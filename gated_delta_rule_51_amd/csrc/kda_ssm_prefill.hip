@@ -208,8 +208,9 @@ __device__ __forceinline__ void run_segment(const SsmArgs &a, const Segments &sg
             *reinterpret_cast<u32x4 *>(lds + C::OFF_C + tile_at<C::PPR>(tid / C::PPR + each * i, tid % C::PPR)) = cr[i];
     };
 
-    // gates, by the last wave of each head, a token a lane
-    const bool gates = active && pc == C::WPH - 1;
+    // gates, by the last wave of each head, a token a lane; an empty sequence has
+    // none, and without any token A_log may be NULL
+    const bool gates = active && len > 0 && pc == C::WPH - 1;
     const double A = uniform(gates ? -exp((double)a.A_log[h]) * 1.4426950408889634 : 0.0);
     const float bias = gates && a.dt_bias ? a.dt_bias[h] : 0.f, Dh = active && a.D ? a.D[h] : 0.f;
     const bf16 *dg = reinterpret_cast<const bf16 *>(a.dt) + (long)t0 * a.dt_stride + h;

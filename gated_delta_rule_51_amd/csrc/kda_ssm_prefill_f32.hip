@@ -106,8 +106,9 @@ __device__ __forceinline__ void run_segment_f32(const SsmArgs &a, const Segments
         }
     };
 
-    // gates, by the last wave of each head, a token a lane
-    const bool gates = active && pc == C::WPH - 1;
+    // gates, by the last wave of each head, a token a lane; an empty sequence has
+    // none, and without any token A_log may be NULL
+    const bool gates = active && len > 0 && pc == C::WPH - 1;
     const double A = uniform(gates ? -exp((double)a.A_log[h]) * 1.4426950408889634 : 0.0);
     const float bias = gates && a.dt_bias ? a.dt_bias[h] : 0.f, Dh = active && a.D ? a.D[h] : 0.f;
     const float *dg = reinterpret_cast<const float *>(a.dt) + (long)t0 * a.dt_stride + h;

@@ -439,6 +439,7 @@ typedef struct {
  *   A_log [H], D [H] or NULL, dt_bias [H] or NULL: fp32
  *   state, state_indices, final_state, cu_seqlens: as for kda_chunk_prefill
  *   y  [T, H, P] io dtype, contiguous; must not overlap any input
+ * With total_tokens 0 the arrays of tokens and A_log may be NULL.
  * Precision: states and sums are fp32, sums of log-decays fp64 (a token's
  * log-decay, in powers of 2, below -1024 counts as that).  kda_ssm_prefill's
  * products run on the matrix cores: with fp32 io on fp32 operands; with bf16 io
