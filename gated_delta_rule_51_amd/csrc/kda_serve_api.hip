@@ -90,10 +90,10 @@ struct SsmIn {
 };
 
 // The checks the three scan calls share, for T tokens; fills `a`.  more: what
-// else is read or written; the states and the cache that are written overlap
-// no input, y overlaps nothing.
+// else is read or written; the states that are written and the cache or the
+// workspace (`extra`) overlap no input, y overlaps nothing.
 kda_status ssm_common(const kda_ssm_desc *d, const SsmIn &in, long T, const void *y, const Range (&more)[5], const Range &states,
-                      const Range &cache, SsmArgs &a) {
+                      const Range &extra, SsmArgs &a) {
     if (T > 0 && (!in.x || !in.dt || !in.A_log || !in.B || !in.C || !y)) return KDA_ERR_NULL;
     const long hp = (long)d->heads * d->head_dim, gs = (long)d->groups * d->state_dim;
     if (in.z && d->z_stride < hp) return KDA_ERR_SHAPE;
@@ -109,7 +109,7 @@ kda_status ssm_common(const kda_ssm_desc *d, const SsmIn &in, long T, const void
                          {in.B, rows_bytes(T, d->b_stride, gs, isz)}, {in.C, rows_bytes(T, d->c_stride, gs, isz)},
                          {in.z, in.z ? rows_bytes(T, d->z_stride, hp, isz) : 0}, {in.A_log, (size_t)d->heads * 4},
                          {in.D, (size_t)d->heads * 4}, {in.dt_bias, (size_t)d->heads * 4}};
-    if (hits(out, ins) || hits(out, more) || hits(states, ins) || hits(cache, ins)) return KDA_ERR_ALIAS;
+    if (hits(out, ins) || hits(out, more) || hits(states, ins) || hits(extra, ins)) return KDA_ERR_ALIAS;
     a = SsmArgs{};
     a.x = in.x; a.dt = in.dt; a.B = in.B; a.C = in.C; a.z = in.z;
     a.A_log = in.A_log; a.D = in.D; a.dt_bias = in.dt_bias;
@@ -241,13 +241,13 @@ kda_status kda_ssm_prefill(const kda_ssm_desc *d, const void *x, const void *dt,
     const Range before{state, ssm_states(d, pool ? d->num_slots : N)}, last{pool ? nullptr : final_state, ssm_states(d, N)};
     const Range more[5] = {before, last, {cu_seqlens, (size_t)(N + 1) * 4}, {state_indices, (size_t)N * 4}, {workspace, need}};
     SsmArgs a;
-    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, T, y, more, pool ? before : last, {}, a);
+    st = ssm_common(d, SsmIn{x, dt, B, C, z, A_log, D, dt_bias}, T, y, more, pool ? before : last, more[4], a);
     if (st != KDA_OK) return st;
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
-    const Range written = pool ? before : last;
-    if (overlap(written.p, written.n, cu_seqlens, more[2].n) || overlap(written.p, written.n, state_indices, more[3].n) ||
-        overlap(written.p, written.n, workspace, need) ||
-        (last.p && last.p != state && overlap(last.p, last.n, state, before.n)))
+    // (the workspace is written while inputs, offsets and first states are still to be read)
+    const Range written = pool ? before : last, offsets[] = {more[2], more[3]};
+    if (hits(written, offsets) || hits(more[4], offsets) || overlap(written.p, written.n, workspace, need) ||
+        overlap(before.p, before.n, workspace, need) || (last.p && last.p != state && overlap(last.p, last.n, state, before.n)))
         return KDA_ERR_ALIAS;
     if (N == 0 || (T == 0 && (pool || !final_state))) return KDA_OK;
     st = grid_ok(ssm_prefill_grid(d->num_seqs, d->total_tokens, d->heads, d->groups, d->head_dim), N);

@@ -440,6 +440,8 @@ typedef struct {
  *   state, state_indices, final_state, cu_seqlens: as for kda_chunk_prefill
  *   y  [T, H, P] io dtype, contiguous; must not overlap any input
  * With total_tokens 0 the arrays of tokens and A_log may be NULL.
+ * The workspace overlaps nothing else; it may be reused by calls that are
+ * ordered on one stream.
  * Precision: states and sums are fp32, sums of log-decays fp64 (a token's
  * log-decay, in powers of 2, below -1024 counts as that).  kda_ssm_prefill's
  * products run on the matrix cores: with fp32 io on fp32 operands; with bf16 io
@@ -506,7 +508,8 @@ typedef struct {
  * The running sums are formed in fp64, so the token found does not depend on
  * how they are split.  A draft outside [0, V) is refused, without a read, and
  * takes no weight from its row.  Probabilities that are NaN or not above zero
- * weigh nothing.  Outputs overlap no input and not one another.
+ * weigh nothing.  Outputs and the workspace overlap no input and not one
+ * another; a workspace may be reused by calls that are ordered on one stream.
  */
 size_t kda_verify_drafts_workspace_size(const kda_verify_desc *desc);
 kda_status kda_verify_drafts(const kda_verify_desc *desc, const int32_t *tokens,
