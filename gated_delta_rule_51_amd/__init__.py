@@ -459,6 +459,8 @@ def _cache_pitch(cache, n, hv, dv, dk, dtype):
         raise ValueError("intermediate_states must be [>= N, steps, Hv, V, K]")
     unit = hv * dv * dk
     st = cache.stride()
+    if unit == 0:
+        raise ValueError("intermediate_states must have heads and rows")
     if st[1:] != (unit, dv * dk, dk, 1) or st[0] % unit != 0 or st[0] // unit < cache.shape[1]:
         raise ValueError("intermediate_states must be contiguous within each request")
     return st[0] // unit

@@ -101,7 +101,7 @@ int32_t sequences(const Tensor &cu) {
 int64_t cache_pitch(const Tensor &t, ScalarType type, int64_t n, int64_t a, int64_t b, int64_t c) {
     const auto size = t.sizes(), step = t.strides();
     const int64_t unit = a * b * c;
-    need(t.scalar_type() == type && size.size() == 5 && size[0] >= n && size[2] == a && size[3] == b && size[4] == c);
+    need(unit > 0 && t.scalar_type() == type && size.size() == 5 && size[0] >= n && size[2] == a && size[3] == b && size[4] == c);
     need(step[1] == unit && step[2] == b * c && step[3] == c && step[4] == 1 && step[0] % unit == 0 && step[0] / unit >= size[1]);
     return step[0] / unit;
 }

@@ -22,3 +22,24 @@ def test_scan_workspace_overlaps_nothing(L, name):  # noqa: F811
     pool = dict(idx=fake(13), state=fake(14), final=None)
     assert ssm(L, long, ws=fake(20), n=need, **dict(pool, idx=fake(20, 64))) == ALIAS
     assert ssm(L, long, ws=fake(20), n=need, **dict(pool, state=fake(20, 4096))) == ALIAS
+
+
+def no_heads(device):
+    """A pool and a step cache of states without heads, whose pitch in steps
+    would be a division by zero."""
+    pool, cache = torch.zeros(4, 0, 64, 64, device=device), torch.zeros(2, 2, 0, 64, 64, device=device)
+    return pool, cache.as_strided((2, 2, 0, 64, 64), (0, 0, 64 * 64, 64, 1)), torch.zeros(2, dtype=torch.int32, device=device)
+
+
+def test_commit_of_no_heads():
+    pool, cache, idx = no_heads("cpu")
+    with pytest.raises(ValueError, match="heads and rows"):
+        kda.commit_states(pool, idx, cache, idx)
+
+
+@pytest.mark.gpu
+def test_commit_of_no_heads_natively():
+    pool, cache, idx = no_heads("cuda")
+    assert kda._native().commit_states(0, pool, idx, cache, idx) is None
+    with pytest.raises(ValueError, match="heads and rows"):
+        kda.commit_states(pool, idx, cache, idx)
