@@ -103,7 +103,9 @@ kda_status ssm_common(const kda_ssm_desc *d, const SsmIn &in, long T, const void
         if (r.p && !aligned(r.p)) return KDA_ERR_ALIGN;
     const size_t isz = io_size(d->io_dtype);
     const long vec = (long)(16 / isz);
-    if (T > 1 && (d->x_stride % vec || d->b_stride % vec || d->c_stride % vec || (in.z && d->z_stride % vec))) return KDA_ERR_ALIGN;
+    if (T > 1 && (d->x_stride % vec || d->b_stride % vec || d->c_stride % vec)) return KDA_ERR_ALIGN;
+    // z comes from a projection beside dt, whose heads may be any number; its loads want whole words
+    if (T > 1 && in.z && d->z_stride * (long)isz % 4) return KDA_ERR_ALIGN;
     const Range out{y, (size_t)T * hp * isz};
     const Range ins[] = {{in.x, rows_bytes(T, d->x_stride, hp, isz)}, {in.dt, rows_bytes(T, d->dt_stride, d->heads, isz)},
                          {in.B, rows_bytes(T, d->b_stride, gs, isz)}, {in.C, rows_bytes(T, d->c_stride, gs, isz)},

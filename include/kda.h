@@ -434,8 +434,8 @@ typedef struct {
  *   x  [T, H, P], dt [T, H], B, C [T, G, S], z [T, H, P] or NULL: io dtype,
  *      token rows *_stride elements apart, contiguous within a row, so that
  *      slices of a projection's or a convolution's rows are read in place;
- *      rows of x, B, C and z lie a multiple of 16 bytes and at most 2^22
- *      elements apart
+ *      rows of x, B and C lie a multiple of 16 bytes apart, of z of 4 bytes,
+ *      and none of these more than 2^22 elements
  *   A_log [H], D [H] or NULL, dt_bias [H] or NULL: fp32
  *   state, state_indices, final_state, cu_seqlens: as for kda_chunk_prefill
  *   y  [T, H, P] io dtype, contiguous; must not overlap any input

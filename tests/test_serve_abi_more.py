@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import gated_delta_rule_51_amd as kda
-from test_serve_abi import ALIAS, L, fake, ssm, ssm_desc  # noqa: F401  (L: fixture)
+from test_serve_abi import ALIAS, ALIGN, L, fake, ssm, ssm_desc  # noqa: F401  (L: fixture)
 
 
 @pytest.mark.parametrize("name", ["x", "dt", "A", "B", "C", "D", "z", "bias", "cu", "state", "final", "y"])
@@ -43,3 +43,10 @@ def test_commit_of_no_heads_natively():
     assert kda._native().commit_states(0, pool, idx, cache, idx) is None
     with pytest.raises(ValueError, match="heads and rows"):
         kda.commit_states(pool, idx, cache, idx)
+
+
+def test_scan_z_rows_of_whole_words(L):  # noqa: F811
+    """Rows of z need not start on 16 bytes, as beside [T, H] steps of any H in
+    one projection: such a call passes that check and gets to the next one."""
+    for io, stride, want in ((1, 258, ALIAS), (1, 266, ALIAS), (1, 259, ALIGN), (0, 257, ALIAS)):
+        assert ssm(L, ssm_desc(io_dtype=io, z_stride=stride), y=fake(7, 512)) == want, (io, stride)
