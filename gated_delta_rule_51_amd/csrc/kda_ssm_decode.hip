@@ -43,12 +43,13 @@ __device__ __forceinline__ void ssm_inputs(const SsmArgs &a, long t, int h, int 
     }
 }
 
-// A head's constants: the rate, the bias of its step and D.
+// A head's constants: the rate (finite, as a step may be 0), the bias of its step
+// and D.
 template <int HD>
 __device__ __forceinline__ void ssm_heads(const SsmArgs &a, int h, float (&A)[HD], float (&bias)[HD], float (&Dh)[HD]) {
 #pragma unroll
     for (int k = 0; k < HD; ++k) {
-        A[k] = -expf(a.A_log[h + k]);
+        A[k] = -fminf(expf(a.A_log[h + k]), 3.4e38f);
         bias[k] = a.dt_bias ? a.dt_bias[h + k] : 0.f;
         Dh[k] = a.D ? a.D[h + k] : 0.f;
     }

@@ -52,3 +52,25 @@ def test_z_from_a_projection(io, wide, P, S):
 
     for a, b in zip(run(z), run(z.contiguous())):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("io", [BF, F32], ids=["bf16", "f32"])
+def test_rate_beyond_fp32(io):
+    """A rate of e^89, above fp32's largest, and steps that are zero in fp32: the
+    decay is 1 (the exponent is below 1e-45), and after a step of 1 it is 0."""
+    H, P, S = 8, 32, 32      # a row of dt is 16 bytes or more, so that every one starts on 16
+    x, B = torch.ones(3, H, P, dtype=io, device="cuda"), torch.ones(3, 1, S, dtype=io, device="cuda")
+    dt = torch.tensor([-200.0, -200.0, 40.0], device="cuda").to(io)[:, None].expand(3, H).contiguous()
+    A = torch.full((H,), 89.0, device="cuda")
+    first = torch.randn(1, H, P, S, device="cuda")
+    idx = torch.zeros(1, dtype=I32, device="cuda")
+    for lens in ([2], [3]):
+        n = lens[0]
+        cut = (x[:n], dt[:n], A, B[:n], B[:n])
+        want = first if n == 2 else torch.full_like(first, 40.0)
+        _, last = kda.ssm_prefill(*cut, offsets(lens), initial_state=first)
+        pool, one = first.clone(), first.clone()
+        kda.ssm_decode_multi(*cut, offsets(lens), pool, idx)
+        for t in range(n):
+            kda.ssm_decode(x[t:t + 1], dt[t:t + 1], A, B[t:t + 1], B[t:t + 1], one, idx)
+        assert torch.equal(last, want) and torch.equal(pool, want) and torch.equal(one, want)
