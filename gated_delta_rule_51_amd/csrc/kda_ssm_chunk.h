@@ -19,7 +19,7 @@ template <typename T> __device__ __forceinline__ T uniform(T x) {
 }
 
 struct Segments {
-    int len;        // tokens, a multiple of 64
+    int len;        // tokens: a multiple of 64, or all of them where every sequence is one segment
     int after;      // floor(T / len): at least the segments after the sequences' first
     bool later;     // the last launch
     // Segment k of sequence n, but for its last, has the place floor(cu[n] / len) + k.

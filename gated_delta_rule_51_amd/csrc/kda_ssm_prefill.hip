@@ -627,15 +627,25 @@ static hipError_t launch_any(const SsmArgs &a, const Segments &sg, hipStream_t s
 }
 
 // Tokens of a segment: as many as leave the chip's 512 resident workgroups
-// about two segments each, at least two chunks, or eight where the sequences
-// by themselves keep half the chip busy (the launches after the first cost
-// more than a shorter chain then saves).  Measured at least 64, 128, 256 and
-// 512 tokens: one prompt of 8,192 x 8 heads (fp32) 117, 99, 137, 230 us; of
-// 600 x 8 heads (bf16) 38, 47, 65, 61; 20 of 400 x 8 heads 73, 74, 54, 61.
+// about two segments each, but at least 64 where the sequences by themselves
+// are fewer than 64 workgroups, 128 below 128 and else 256 (the launches after
+// the first cost more than a shorter chain then saves).  Measured (us) at
+// least, S = 128:
+//     workgroups                                   64     128     256     512
+//      4  1 x 600, 8 heads x 64 (bf16 / fp32)  29 / 60  40 / 98  58 / 171  66 / 207
+//      8  1 x 4096, 8 x 128 (bf16)                 54      50      62      95
+//     16  8 x 1000, 4 x 64 (bf16)                  40      46      63     102
+//     28  7 x 1 .. 300, 8 x 64, S = 64 (fp32)      40      60      56      55
+//     64  4 x 512, 32 x 64 (bf16 / fp32)     48 / 101 47 / 107 62 / 179 54 / 171
+//     80  20 x 400, 8 x 64 (bf16 / fp32)     50 / 109 48 / 109 58 / 160 50 / 151
+//    100  100 x 130, 1 x 128 (bf16 / fp32)    36 / 62  35 / 74  28 / 66  28 / 66
+//    120  60 x 500, 4 x 64 (bf16)                  80      60      65      57
+//    128  8 x 1000, 32 x 64 (bf16 / fp32)    99 / 304 99 / 304 84 / 277 106 / 339
+//    320  20 x 130, 32 x 64 (bf16 / fp32)    68 / 168 52 / 161 42 / 142 43 / 142
 static Segments segments_of(int num_seqs, int total_tokens, int head_workgroups) {
     Segments sg{};
     const long len = ((long)total_tokens * head_workgroups / 1024 + 63) / 64 * 64;
-    const long least = (long)num_seqs * head_workgroups >= 128 ? 512 : 128;
+    const long alone = (long)num_seqs * head_workgroups, least = alone < 64 ? 64 : alone < 128 ? 128 : 256;
     sg.len = (int)std::min(std::max(len, least), (long)INT32_MAX - 63);
     const bool single = sg.len >= total_tokens;   // every sequence is one segment
     if (single) sg.len = total_tokens > 0 ? total_tokens : 1;
