@@ -655,6 +655,8 @@ def _conv_args(x, weight, bias):
         raise ValueError("x must be [T, D]")
     _io_dtype(x)
     T, D = x.shape
+    if weight.dim() == 2 and not 2 <= weight.shape[1] <= 4:
+        raise ValueError("weight must have 2 to 4 taps, got %d" % weight.shape[1])
     if not (weight.dtype is x.dtype and weight.dim() == 2 and weight.shape[0] == D and weight.is_contiguous()):
         _need(weight, "weight", x.dtype, 2)
         raise ValueError("weight must have shape [%d, W], got %s" % (D, tuple(weight.shape)))
@@ -735,7 +737,9 @@ def _ssm_desc(x, dt, A_log, B, C, D, z, dt_bias, num_seqs, state_dtype):
         raise ValueError("B must be [T, G, S]")
     T, H, P = x.shape
     G, S = B.shape[1], B.shape[2]
-    if G <= 0 or H % G != 0:
+    if min(H, P, G, S) <= 0:
+        raise ValueError("x [T, H, P] and B [T, G, S] must have heads, groups and states, got %s and %s" % (tuple(x.shape), tuple(B.shape)))
+    if H % G != 0:
         raise ValueError("heads (%d) must be a multiple of groups (%d)" % (H, G))
     if state_dtype not in _DT:
         raise ValueError("states must be float32 or bfloat16")
@@ -825,6 +829,8 @@ def verify_drafts(tokens, target_probs, cu_seqlens, uniform, uniform_next, *, dr
         raise ValueError("target_probs must be [T, V]")
     if target_probs.dtype not in _DT:
         raise ValueError("target_probs must be float32 or bfloat16")
+    if target_probs.shape[1] == 0:
+        raise ValueError("target_probs must have a vocabulary")
     N, T, V = _cu(cu_seqlens), tokens.shape[0], target_probs.shape[1]
     _token_rows(target_probs, "target_probs", target_probs.dtype, T, (V,))
     if draft_probs is not None:

@@ -50,3 +50,20 @@ def test_scan_z_rows_of_whole_words(L):  # noqa: F811
     one projection: such a call passes that check and gets to the next one."""
     for io, stride, want in ((1, 258, ALIAS), (1, 266, ALIAS), (1, 259, ALIGN), (0, 257, ALIAS)):
         assert ssm(L, ssm_desc(io_dtype=io, z_stride=stride), y=fake(7, 512)) == want, (io, stride)
+
+
+def test_empty_sizes_are_named():
+    """What the native call declines for its sizes is named, not called a tensor
+    of a strange kind."""
+    i32, z = torch.int32, torch.zeros
+    cu, idx = torch.tensor([0, 4], dtype=i32), z(4, dtype=i32)
+    x, X = z(4, 8), z(4, 2, 32)
+    for call, msg in (
+            (lambda: kda.conv_prefill(x, z(8, 0), None, cu), "2 to 4 taps"),
+            (lambda: kda.conv_decode(x, z(8, 5), None, z(2, 4, 8), idx), "2 to 4 taps"),
+            (lambda: kda.ssm_prefill(z(4, 0, 32), z(4, 0), z(0), z(4, 1, 32), z(4, 1, 32), cu), "must have heads"),
+            (lambda: kda.ssm_decode(X, z(4, 2), z(2), z(4, 1, 0), z(4, 1, 0), z(5, 2, 32, 0), idx), "must have heads"),
+            (lambda: kda.ssm_prefill(X, z(4, 2), z(2), z(4, 0, 32), z(4, 0, 32), cu), "must have heads"),
+            (lambda: kda.verify_drafts(idx, z(4, 0), cu, z(4), z(1)), "vocabulary")):
+        with pytest.raises(ValueError, match=msg):
+            call()
