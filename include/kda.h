@@ -448,7 +448,10 @@ typedef struct {
  * on bf16 operands, x, B and C as they are and every fp32 factor as the sum of
  * three bf16 terms, which hold all its bits.  The other entry points compute in
  * fp32.
- * Not checked: inputs are finite.
+ * Not checked: inputs are finite.  In kda_ssm_prefill an infinity or NaN in x also
+ * makes NaN of its column in up to 31 tokens before it (those of the same 32,
+ * counted from the sequence's first token or a segment's), as the products run
+ * over all of them; the other entry points take tokens one by one.
  */
 size_t kda_ssm_prefill_workspace_size(const kda_ssm_desc *desc);
 kda_status kda_ssm_prefill(const kda_ssm_desc *desc, const void *x, const void *dt,
@@ -505,10 +508,13 @@ typedef struct {
  *               above zero, or for a request with no tokens
  *   emitted     [T] int32, in the request's rows: the drafts that stood, the
  *               next token, then -1
- * The running sums are formed in fp64, so the token found does not depend on
- * how they are split.  A draft outside [0, V) is refused, without a read, and
- * takes no weight from its row.  Probabilities that are NaN or not above zero
- * weigh nothing.  Outputs and the workspace overlap no input and not one
+ * The running sums are formed in fp64, in parts and an order that depend on V
+ * alone: the token is the same from call to call, whatever the other requests.
+ * It is that of exact sums but where uniform_next[n] times the total lies within
+ * fp64's rounding of a running sum.  A draft outside [0, V) is refused, without
+ * a read, and takes no weight from its row.  A token whose p, or p - q where q is
+ * taken off, is NaN or not above zero weighs nothing.  Not checked:
+ * probabilities are not infinite.  Outputs and the workspace overlap no input and not one
  * another; a workspace may be reused by calls that are ordered on one stream.
  */
 size_t kda_verify_drafts_workspace_size(const kda_verify_desc *desc);

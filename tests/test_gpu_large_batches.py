@@ -110,3 +110,21 @@ def test_parts_of_several_steps(V, with_q, dtype):
     p, q, tokens, u, r = make(V, lens, V, dtype)
     r[-1], r[-2] = 1 - 2.0 ** -24, 0.0
     check(kda, lens, p, q if with_q else None, tokens, u, r)
+
+
+@pytest.mark.parametrize("V", [20001, 40001])
+def test_token_whatever_the_batch(V):
+    """Random numbers on and next to the borders of the running sums: a request
+    among 300 (rows summed by one workgroup at the smaller V) finds the token that
+    it finds alone (by several, with a second launch)."""
+    g = torch.Generator().manual_seed(V)
+    p = torch.softmax(2.5 * torch.randn(1, V, generator=g), 1)
+    cum = p.double().cumsum(1)[0]
+    r = (cum[torch.randint(0, V - 1, (100,), generator=g)] / cum[-1]).float()
+    r = torch.cat([r, torch.nextafter(r, torch.zeros(())), torch.nextafter(r, torch.ones(()))]).clamp(0, 1 - 2.0 ** -24)
+    n = len(r)
+    tokens, u = torch.zeros(n, dtype=I32, device="cuda"), torch.zeros(n, device="cuda")
+    many = kda.verify_drafts(tokens, p.expand(n, V).contiguous().cuda(), offsets([1] * n), u, r.cuda())[1]
+    one = p.cuda()
+    alone = [kda.verify_drafts(tokens[:1], one, offsets([1]), u[:1], x.clone())[1] for x in r.cuda().split(1)]
+    assert torch.equal(many, torch.cat(alone))

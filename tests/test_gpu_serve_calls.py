@@ -74,3 +74,22 @@ def test_rate_beyond_fp32(io):
         for t in range(n):
             kda.ssm_decode(x[t:t + 1], dt[t:t + 1], A, B[t:t + 1], B[t:t + 1], one, idx)
         assert torch.equal(last, want) and torch.equal(pool, want) and torch.equal(one, want)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_one_bad_input(bad):
+    """An infinity or NaN in x at one token spoils its column from that token's
+    32 on, not the tokens before, nor other columns or sequences."""
+    H, P, S, lens, at = 2, 64, 64, [200, 50], 101
+    m = Layer(9, sum(lens), H, P, S, 1, BF)
+    want, ends = kda.ssm_prefill(*m.args, offsets(lens), **m.kw)
+    x = m.args[0].clone()
+    x[at, 1, 5] = bad
+    y, last = kda.ssm_prefill(x, *m.args[1:], offsets(lens), **m.kw)
+    assert not bool(y[at:200, 1, 5].isfinite().any())
+    some = torch.ones_like(y, dtype=torch.bool)
+    some[at // 32 * 32:200, 1, 5] = False
+    assert torch.equal(y[some], want[some])
+    ok = torch.ones_like(last, dtype=torch.bool)
+    ok[0, 1, 5] = False
+    assert torch.equal(last[ok], ends[ok])
