@@ -8,8 +8,8 @@
 // total is found from the sums, and only that part is read again to find the
 // token.  Bound by those rows' bytes with many requests, by the chain of
 // dependent loads with one.  Measured: 1024 requests with rows of 65,536 (fp32,
-// runs of four, 0.43 GB) 88 us, 4.9 TB/s; one request, 131,072 tokens: 10.7 us
-// (4.7 the sums, 3.9 the token, two launches).
+// runs of four, 0.43 GB) 88 us, 4.9 TB/s; one request, 131,072 tokens: 11 us
+// (4.9 the sums, 3.6 the token, two launches).
 #include "kda_device.h"
 #include "kda_internal.h"
 

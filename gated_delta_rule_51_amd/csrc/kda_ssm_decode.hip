@@ -9,7 +9,7 @@
 // once and written once with 16-byte nontemporal accesses.
 //
 // Measured: one token of 4096 requests x 32 heads x (128 x 128) 3.00 ms
-// (17.3 GB, 5.8 TB/s); of one request 4.2 us, a launch and a row's latency; four
+// (17.3 GB, 5.8 TB/s); of one request 4.3 us, a launch and a row's latency; four
 // tokens of 1024 requests x 32 heads x (64 x 128), every state cached, 0.93 ms
 // (5.4 GB, 5.8 TB/s, four fifths of it writes).
 #include "kda_device.h"

@@ -39,9 +39,13 @@
 // What bounds it.  At P = S = 128 a wave's chunk takes 122 products of 32
 // cycles and about 1200 vector instructions of 4, two waves a SIMD, most of them
 // the splitting of fp32 operands, the gating by z and M's exponentials, so the
-// vector units set the pace; memory is at 1.8 TB/s.  16 prompts of 512 to 4096
-// tokens x 32 heads x (128 x 128): 375 to 390 us by the run (0.69 GB, 64 GFLOP);
-// one of 32,768 x 32 heads x (64 x 128), gated: 287 to 294 us.
+// vector units set the pace: they issue in 51 to 60% of the busy CUs' cycles, the
+// matrix cores are busy in 41 to 36%, and the tails of two launches leave 17 to
+// 27% of the CUs without work.  Memory is at 1.8 TB/s.  16 prompts of 512 to 4096
+// tokens x 32 heads x (128 x 128): 375 to 400 us by the run (0.69 GB, 64 GFLOP);
+// one of 32,768 x 32 heads x (64 x 128), gated: 287 to 295 us, of which the first
+// launch takes about 95 and the carry 22.  Held back by registers: P = S = 128
+// spills 20, P = 32 with S = 128 55.
 #include <algorithm>
 #include <type_traits>
 
