@@ -36,6 +36,16 @@ anything else.  The calls beside the delta rule go through a native module
     commit_states(state_pool, state_indices, cache, accepted)     # either decode's step cache
     conv_commit(x, cu_seqlens, accepted, conv_pool, state_indices)
 
+    # layers of attention between the recurrent ones: blocks and slots, 8-bit keys and values, attention over them
+    slots, totals = kv_reserve(cu_seqlens, T, state_indices, kv_lens, blocks_held, block_table, free_blocks, free_count, block_size=64)
+    kv_store(k, v, slots, k_cache, v_cache, k_scale, v_scale)                       # every layer
+    o = kv_attention(q, cu_seqlens, totals, state_indices, block_table, k_cache, v_cache, k_scale, v_scale)
+    kv_commit(cu_seqlens, state_indices, kv_lens, blocks_held, block_size=64)       # or steps=accepted
+    kv_release(state_indices, kv_lens, blocks_held, block_table, free_blocks, free_count, block_size=64)
+    # the next token, and the probabilities that verify_drafts takes
+    tokens = sample_tokens(logits, uniform, temperature=t, top_k=k, top_p=p, min_p=m)
+    probs = token_probs(logits, temperature=t, top_k=k, top_p=p, min_p=m)
+
 Layouts (contiguous): q, k [T, Hk, K]; v [T, Hv, V]; g [T, Hv, K] (per-channel
 gate) or [T, Hv] (scalar gate); beta [T, Hv] fp32; states [.., Hv, V, K];
 raw x shaped like g and b like beta, both in the io dtype; A_log, dt_bias
@@ -53,6 +63,7 @@ __all__ = ["chunk_prefill", "chunk_prefill_noalloc", "recurrent_decode", "chunk_
            "recurrent_decode_packed", "recurrent_decode_packed_fused_gate",
            "conv_prefill", "conv_decode", "conv_commit", "ssm_prefill", "ssm_decode", "ssm_decode_multi",
            "verify_drafts", "commit_states",
+           "kv_reserve", "kv_commit", "kv_release", "kv_store", "kv_attention", "sample_tokens", "token_probs",
            "workspace_size", "release_workspaces", "library_path", "KdaError"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -127,6 +138,27 @@ class CommitDesc(ctypes.Structure):
                 ("row_bytes", ctypes.c_int64)]
 
 
+class PagesDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_free", ctypes.c_int32)]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class SampleDesc(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("logits_dtype", ctypes.c_int32), ("stride", ctypes.c_int64)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 
@@ -182,6 +214,22 @@ def lib():
         L.kda_verify_drafts.argtypes = [ctypes.POINTER(VerifyDesc)] + [_P] * 10 + [ctypes.c_size_t, _P]
         L.kda_commit_states.restype = ctypes.c_int
         L.kda_commit_states.argtypes = [ctypes.POINTER(CommitDesc)] + [_P] * 5
+        L.kda_kv_reserve.restype = ctypes.c_int
+        L.kda_kv_reserve.argtypes = [ctypes.POINTER(PagesDesc)] + [_P] * 10
+        L.kda_kv_commit.restype = ctypes.c_int
+        L.kda_kv_commit.argtypes = [ctypes.POINTER(PagesDesc)] + [_P] * 6
+        L.kda_kv_release.restype = ctypes.c_int
+        L.kda_kv_release.argtypes = [ctypes.POINTER(PagesDesc)] + [_P] * 8
+        L.kda_kv_store.restype = ctypes.c_int
+        L.kda_kv_store.argtypes = [ctypes.POINTER(KvDesc)] + [_P] * 8
+        L.kda_kv_attention_workspace_size.restype = ctypes.c_size_t
+        L.kda_kv_attention_workspace_size.argtypes = [ctypes.POINTER(KvDesc)]
+        L.kda_kv_attention.restype = ctypes.c_int
+        L.kda_kv_attention.argtypes = [ctypes.POINTER(KvDesc)] + [_P] * 11 + [ctypes.c_size_t, _P]
+        L.kda_sample_tokens_workspace_size.restype = ctypes.c_size_t
+        L.kda_sample_tokens_workspace_size.argtypes = [ctypes.POINTER(SampleDesc)]
+        L.kda_sample_tokens.restype = ctypes.c_int
+        L.kda_sample_tokens.argtypes = [ctypes.POINTER(SampleDesc)] + [_P] * 9 + [ctypes.c_size_t, _P]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_version.restype = ctypes.c_int32
@@ -555,7 +603,7 @@ def recurrent_decode_packed_fused_gate(qkv, gate_x, A_log, dt_bias, beta_x, stat
                           scale, True)
 
 
-# ---- short causal convolution, state-space scan, drafts ---------------------
+# ---- short causal convolution, state-space scan, drafts; paged cache, tokens -
 
 
 # A one-token step takes a few microseconds on the GPU, so the checks, outputs
@@ -856,3 +904,184 @@ def commit_states(state_pool, state_indices, intermediate_states, steps):
         raise ValueError("commit_states needs the step cache")
     _cache_pitch(intermediate_states, N, *one, state_pool.dtype)
     _declined(state_pool, (state_indices, intermediate_states, steps))
+
+
+# ---- paged cache and the next token ------------------------------------------
+
+
+def _block_size(block_size):
+    if block_size not in (16, 32, 64, 128):
+        raise ValueError("block_size must be 16, 32, 64 or 128, got %r" % (block_size,))
+    return int(block_size)
+
+
+def _exactly(t, name, dtype, shape):
+    _need(t, name, dtype, len(shape))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+def _pages(state_indices, n, kv_lens, blocks_held, block_table, free_blocks, free_count):
+    _whole(state_indices, "state_indices", torch.int32, n, ())
+    _need(block_table, "block_table", torch.int32, 2)
+    rows = block_table.shape[0]
+    if min(block_table.shape) < 1:
+        raise ValueError("block_table must have rows and entries, got %s" % (tuple(block_table.shape),))
+    _exactly(kv_lens, "kv_lens", torch.int32, (rows,))
+    _exactly(blocks_held, "blocks_held", torch.int32, (rows,))
+    _need(free_blocks, "free_blocks", torch.int32, 1)
+    _exactly(free_count, "free_count", torch.int32, (1,))
+
+
+def kv_reserve(cu_seqlens, total_tokens, state_indices, kv_lens, blocks_held, block_table, free_blocks, free_count, *,
+               block_size):
+    """Blocks and slots for the tokens to come.  Request n, on row
+    state_indices[n] of kv_lens, blocks_held [rows] and block_table [rows,
+    max_blocks], holds kv_lens[row] tokens and brings cu_seqlens[n + 1] -
+    cu_seqlens[n] more; the blocks it lacks come off the stack free_blocks
+    [num_free] (free_count [1] of them are there) in the batch's order, none from
+    the first request on whose blocks are not there.  All int32.  Returns (slots
+    [total_tokens], kv_totals [N]): -1 and 0 for requests without their blocks
+    and for padding (an index outside the rows).  kv_lens stays: kv_commit counts
+    the tokens."""
+    block_size = _block_size(block_size)
+    total_tokens = int(total_tokens)
+    if total_tokens < 0:
+        raise ValueError("total_tokens must not be negative")
+    out = _run("kv_reserve", cu_seqlens, total_tokens, state_indices, kv_lens, blocks_held, block_table, free_blocks, free_count,
+               block_size)
+    if out is not None:
+        return out
+    N = _cu(cu_seqlens)
+    _pages(state_indices, N, kv_lens, blocks_held, block_table, free_blocks, free_count)
+    _declined(cu_seqlens, (state_indices, kv_lens, blocks_held, block_table, free_blocks, free_count))
+
+
+def kv_commit(cu_seqlens, state_indices, kv_lens, blocks_held, *, block_size, steps=None):
+    """The requests' new tokens count: kv_lens[row] grows by all of them, or with
+    steps [N] (verify_drafts' accepted) by steps[n] + 1; left as it is where that is
+    not among the request's tokens or beyond its blocks."""
+    block_size = _block_size(block_size)
+    if _run("kv_commit", cu_seqlens, steps, state_indices, kv_lens, blocks_held, block_size):
+        return
+    N = _cu(cu_seqlens)
+    _whole(state_indices, "state_indices", torch.int32, N, ())
+    _whole(kv_lens, "kv_lens", torch.int32, 1, ())
+    _exactly(blocks_held, "blocks_held", torch.int32, tuple(kv_lens.shape))
+    _whole(steps, "steps", torch.int32, N, ())
+    _declined(cu_seqlens, (state_indices, kv_lens, blocks_held, steps))
+
+
+def kv_release(state_indices, kv_lens, blocks_held, block_table, free_blocks, free_count, *, block_size, keep_lens=None):
+    """Requests give back the blocks that their first keep_lens[n] tokens (None:
+    none, they end) do not reach; kv_lens[row] becomes at most that."""
+    block_size = _block_size(block_size)
+    if _run("kv_release", state_indices, kv_lens, blocks_held, block_table, free_blocks, free_count, block_size, keep_lens):
+        return
+    _whole(state_indices, "state_indices", torch.int32, 0, ())
+    N = state_indices.shape[0]
+    _pages(state_indices, N, kv_lens, blocks_held, block_table, free_blocks, free_count)
+    _whole(keep_lens, "keep_lens", torch.int32, N, ())
+    _declined(state_indices, (kv_lens, blocks_held, block_table, free_blocks, free_count, keep_lens))
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale):
+    """Shapes of a cache: (blocks, Hk, block_size, D)."""
+    f8 = torch.float8_e4m3fn
+    _need(k_cache, "k_cache", f8, 4)
+    B, H, bs, D = k_cache.shape
+    if min(B, H) < 1:
+        raise ValueError("k_cache must have blocks and heads, got %s" % (tuple(k_cache.shape),))
+    _block_size(bs)
+    if D not in (64, 128):
+        raise ValueError("the cache's head dim must be 64 or 128, got %d" % D)
+    _exactly(v_cache, "v_cache", f8, (B, H, D, bs))
+    _exactly(k_scale, "k_scale", torch.float32, (B, H))
+    _exactly(v_scale, "v_scale", torch.float32, (B, H))
+    return B, H, bs, D
+
+
+def kv_store(k, v, slots, k_cache, v_cache, k_scale, v_scale):
+    """Keys and values [T, Hk, D] (token rows may lie apart) into the cache, in 8
+    bits with one power-of-two scale a block and head: k_cache [blocks, Hk,
+    block_size, D] and v_cache [blocks, Hk, D, block_size] float8_e4m3fn, k_scale
+    and v_scale [blocks, Hk] fp32.  slots [T] int32 (kv_reserve's; -1: nowhere):
+    consecutive tokens on consecutive slots of a block are a run, and a block takes
+    one run in a call.  Its scale grows where the run needs it, and what the block
+    holds before the run is then stored again under it."""
+    if _run("kv_store", k, v, slots, k_cache, v_cache, k_scale, v_scale):
+        return
+    _io_dtype(k)
+    _, H, _, D = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _whole(slots, "slots", torch.int32, 0, ())
+    T = slots.shape[0]
+    _token_rows(k, "k", k.dtype, T, (H, D))
+    _token_rows(v, "v", k.dtype, T, (H, D))
+    _declined(k, (v, slots, k_cache, v_cache, k_scale, v_scale))
+
+
+def kv_attention(q, cu_seqlens, kv_totals, state_indices, block_table, k_cache, v_cache, k_scale, v_scale, *, scale=None):
+    """Causal attention of every request's new tokens over all of its tokens in the
+    cache (kv_store puts the new ones there first): token j of L stands at position
+    kv_totals[n] - L + j and sees those up to it.  q [T, Hq, D] (token rows may lie
+    apart), Hq a multiple of the cache's heads; kv_totals [N] as kv_reserve gives
+    them; block_table [rows, max_blocks], state_indices [N]; scale: D^-1/2 unless
+    given, above 0.  Returns o [T, Hq, D]; a token that sees nothing gives zeros."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5 if q.dim() and q.shape[-1] else 1.0
+    scale = float(scale)
+    if not 0.0 < scale <= 2.0 ** 20:
+        raise ValueError("scale must lie in (0, 2^20], got %r" % scale)
+    o = _run("kv_attention", q, cu_seqlens, kv_totals, state_indices, block_table, k_cache, v_cache, k_scale, v_scale, scale)
+    if o is not None:
+        return o
+    _io_dtype(q)
+    _, H, _, D = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    if q.shape[1] < 1 or q.shape[1] % H != 0:
+        raise ValueError("query heads (%d) must be a multiple of the cache's (%d)" % (q.shape[1], H))
+    _token_rows(q, "q", q.dtype, q.shape[0], (q.shape[1], D))
+    N = _cu(cu_seqlens)
+    _whole(kv_totals, "kv_totals", torch.int32, N, ())
+    _whole(state_indices, "state_indices", torch.int32, N, ())
+    _need(block_table, "block_table", torch.int32, 2)
+    if min(block_table.shape) < 1:
+        raise ValueError("block_table must have rows and entries, got %s" % (tuple(block_table.shape),))
+    _declined(q, (cu_seqlens, kv_totals, state_indices, block_table, k_cache, v_cache, k_scale, v_scale))
+
+
+def _sample(logits, uniform, temperature, top_k, top_p, min_p, draws, probs):
+    out = _run("sample_tokens", logits, uniform, temperature, top_k, top_p, min_p, draws, probs)
+    if out is not None:
+        return out
+    if logits.dim() != 2 or logits.shape[1] == 0:
+        raise ValueError("logits must be [N, V] with a vocabulary")
+    if logits.dtype not in _DT:
+        raise ValueError("logits must be float32 or bfloat16")
+    N, V = logits.shape
+    _token_rows(logits, "logits", logits.dtype, N, (V,))
+    if draws and uniform is None:
+        raise ValueError("sample_tokens needs uniform")
+    for t, name, dtype in ((uniform, "uniform", torch.float32), (temperature, "temperature", torch.float32),
+                           (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
+        _whole(t, name, dtype, N, ())
+    _declined(logits, (uniform, temperature, top_k, top_p, min_p))
+
+
+def sample_tokens(logits, uniform, *, temperature=None, top_k=None, top_p=None, min_p=None, return_probs=False):
+    """The next token of every row of logits [N, V] (rows may lie apart), from the
+    random numbers uniform [N] fp32 in [0, 1): with w = exp((x - max x) /
+    temperature), the first index at which the running sum passes uniform times the
+    sum, over the weights that top_k, then top_p, then min_p keep.  Each limit is
+    None (temperature 1, everything kept) or has an entry a row: temperature, top_p,
+    min_p [N] fp32, top_k [N] int32; a temperature of 0 takes the largest logit.
+    Returns tokens [N] int32 (-1: no logit), with return_probs also the
+    probabilities [N, V] fp32."""
+    return _sample(logits, uniform, temperature, top_k, top_p, min_p, True, bool(return_probs))
+
+
+def token_probs(logits, *, temperature=None, top_k=None, top_p=None, min_p=None):
+    """The probabilities [N, V] fp32 that sample_tokens draws from: what
+    verify_drafts takes as target_probs and draft_probs."""
+    return _sample(logits, None, temperature, top_k, top_p, min_p, False, True)

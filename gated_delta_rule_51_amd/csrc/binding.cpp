@@ -1,5 +1,4 @@
-// The Python calls of the convolution, scan, verification and commit in native
-// code: argument checks, output allocation and the C call in one step, since
+// The Python calls beside the delta rule's in native code: argument checks, output allocation and the C call in one step, since
 // around a one-token kernel of a few microseconds the same work in Python costs
 // twice the kernel.  A call whose arguments do not all fit is declined (None),
 // and the Python function, which makes the same checks one by one, says why.
@@ -54,6 +53,19 @@ struct Args {
     bool flag(int i) {
         need(PyBool_Check(v[i]));
         return v[i] == Py_True;
+    }
+    double number(int i) {
+        need(PyFloat_Check(v[i]));
+        return PyFloat_AS_DOUBLE(v[i]);
+    }
+    int64_t integer(int i) {
+        need(PyLong_Check(v[i]));
+        const long long n = PyLong_AsLongLong(v[i]);
+        if (n == -1 && PyErr_Occurred()) {   // beyond 64 bits
+            PyErr_Clear();
+            need(false);
+        }
+        return n;
     }
     void *stream() { return PyLong_AsVoidPtr(v[0]); }
 };
@@ -319,6 +331,153 @@ PyObject *commit_states(Args &a) {
     return done(kda_commit_states(&d, ptr(pool), ptr<int32_t>(idx), ptr(cache), ptr<int32_t>(steps), a.stream()));
 }
 
+// The tensors of a block table's state at `i`: kv_lens, blocks_held,
+// block_table, free_blocks, free_count, and the descriptor they make.
+kda_pages_desc pages_desc(Args &a, int i, int64_t n, int64_t block_size) {
+    const Tensor &table = a.tensor(i + 2), &free = a.tensor(i + 3);
+    need(table.dim() == 2);
+    kda_pages_desc d{};
+    d.num_seqs = narrow(n);
+    d.rows = narrow(table.size(0));
+    d.max_blocks = narrow(table.size(1));
+    d.block_size = narrow(block_size);
+    d.num_free = narrow(free.dim() == 1 ? free.size(0) : -1);
+    whole(table, at::kInt, 1, {d.max_blocks});
+    need(d.max_blocks > 0);
+    whole(free, at::kInt, 0, {});
+    exactly(&a.tensor(i), at::kInt, {d.rows});
+    exactly(&a.tensor(i + 1), at::kInt, {d.rows});
+    exactly(&a.tensor(i + 4), at::kInt, {1});
+    return d;
+}
+
+// kv_reserve(stream, cu, total_tokens, indices, kv_lens, held, table, free, count, block_size)
+PyObject *kv_reserve(Args &a) {
+    const Tensor &cu = a.tensor(1), &idx = a.tensor(3);
+    kda_pages_desc d = pages_desc(a, 4, sequences(cu), a.integer(9));
+    d.total_tokens = narrow(a.integer(2));
+    whole(idx, at::kInt, d.num_seqs, {});
+    const Tensor slots = fresh(cu, {d.total_tokens}, at::kInt), totals = fresh(cu, {d.num_seqs}, at::kInt);
+    const kda_status s = kda_kv_reserve(&d, ptr<int32_t>(cu), ptr<int32_t>(idx), ptr<int32_t>(a.tensor(4)), ptr<int32_t>(a.tensor(5)),
+                                        ptr<int32_t>(a.tensor(6)), ptr<int32_t>(a.tensor(7)), ptr<int32_t>(a.tensor(8)), ptr<int32_t>(slots),
+                                        ptr<int32_t>(totals), a.stream());
+    return done(s, slots, nullptr, totals);
+}
+
+// kv_commit(stream, cu, steps, indices, kv_lens, held, block_size)
+PyObject *kv_commit(Args &a) {
+    const Tensor &cu = a.tensor(1), &idx = a.tensor(3), &lens = a.tensor(4), &held = a.tensor(5);
+    const Tensor *steps = a.maybe(2);
+    kda_pages_desc d{};
+    d.num_seqs = sequences(cu);
+    whole(lens, at::kInt, 1, {});
+    d.rows = narrow(lens.size(0));
+    d.block_size = narrow(a.integer(6));
+    exactly(&held, at::kInt, {d.rows});
+    whole(idx, at::kInt, d.num_seqs, {});
+    if (steps) whole(*steps, at::kInt, d.num_seqs, {});
+    return done(kda_kv_commit(&d, ptr<int32_t>(cu), ptr<int32_t>(steps), ptr<int32_t>(idx), ptr<int32_t>(lens), ptr<int32_t>(held), a.stream()));
+}
+
+// kv_release(stream, indices, kv_lens, held, table, free, count, block_size, keep)
+PyObject *kv_release(Args &a) {
+    const Tensor &idx = a.tensor(1);
+    const Tensor *keep = a.maybe(8);
+    whole(idx, at::kInt, 0, {});
+    kda_pages_desc d = pages_desc(a, 2, idx.size(0), a.integer(7));
+    if (keep) whole(*keep, at::kInt, d.num_seqs, {});
+    return done(kda_kv_release(&d, ptr<int32_t>(keep), ptr<int32_t>(idx), ptr<int32_t>(a.tensor(2)), ptr<int32_t>(a.tensor(3)),
+                               ptr<int32_t>(a.tensor(4)), ptr<int32_t>(a.tensor(5)), ptr<int32_t>(a.tensor(6)), a.stream()));
+}
+
+// k_cache, v_cache, k_scale, v_scale at `i`: the cache part of a descriptor.
+kda_kv_desc kv_desc(Args &a, int i) {
+    const Tensor &kc = a.tensor(i), &vc = a.tensor(i + 1), &ks = a.tensor(i + 2), &vs = a.tensor(i + 3);
+    need(kc.dim() == 4);
+    const int64_t B = kc.size(0), H = kc.size(1), bs = kc.size(2), D = kc.size(3);
+    need(B > 0 && H > 0 && bs > 0 && D > 0);
+    exactly(&kc, at::kFloat8_e4m3fn, {B, H, bs, D});
+    exactly(&vc, at::kFloat8_e4m3fn, {B, H, D, bs});
+    exactly(&ks, at::kFloat, {B, H});
+    exactly(&vs, at::kFloat, {B, H});
+    kda_kv_desc d{};
+    d.num_blocks = narrow(B);
+    d.kv_heads = narrow(H);
+    d.block_size = narrow(bs);
+    d.head_dim = narrow(D);
+    return d;
+}
+
+// kv_store(stream, k, v, slots, k_cache, v_cache, k_scale, v_scale)
+PyObject *kv_store(Args &a) {
+    const Tensor &k = a.tensor(1), &v = a.tensor(2), &slots = a.tensor(3);
+    kda_kv_desc d = kv_desc(a, 4);
+    whole(slots, at::kInt, 0, {});
+    const ScalarType io = k.scalar_type();
+    d.io_dtype = code(io);
+    d.total_tokens = narrow(slots.size(0));
+    d.k_stride = rows(k, io, slots.size(0), d.kv_heads, d.head_dim);
+    d.v_stride = rows(v, io, slots.size(0), d.kv_heads, d.head_dim);
+    return done(kda_kv_store(&d, ptr(k), ptr(v), ptr<int32_t>(slots), ptr(a.tensor(4)), ptr(a.tensor(5)), ptr<float>(a.tensor(6)),
+                             ptr<float>(a.tensor(7)), a.stream()));
+}
+
+// kv_attention(stream, q, cu, totals, indices, table, k_cache, v_cache, k_scale, v_scale, scale)
+PyObject *kv_attention(Args &a) {
+    const Tensor &q = a.tensor(1), &cu = a.tensor(2), &totals = a.tensor(3), &idx = a.tensor(4), &table = a.tensor(5);
+    kda_kv_desc d = kv_desc(a, 6);
+    need(q.dim() == 3 && table.dim() == 2);
+    const ScalarType io = q.scalar_type();
+    const int64_t T = q.size(0), H = q.size(1);
+    need(H > 0 && H % d.kv_heads == 0);
+    d.io_dtype = code(io);
+    d.num_seqs = sequences(cu);
+    d.total_tokens = narrow(T);
+    d.q_heads = narrow(H);
+    d.rows = narrow(table.size(0));
+    d.max_blocks = narrow(table.size(1));
+    d.scale = (float)a.number(10);
+    d.q_stride = rows(q, io, T, H, d.head_dim);
+    whole(table, at::kInt, 1, {d.max_blocks});
+    need(d.max_blocks > 0);
+    whole(totals, at::kInt, d.num_seqs, {});
+    whole(idx, at::kInt, d.num_seqs, {});
+    const Tensor o = fresh(q, q.sizes(), io);
+    const size_t bytes = kda_kv_attention_workspace_size(&d);
+    const Tensor ws = bytes ? fresh(q, {(int64_t)bytes}, at::kByte) : Tensor();
+    return done(kda_kv_attention(&d, ptr(q), ptr<int32_t>(cu), ptr<int32_t>(totals), ptr<int32_t>(idx), ptr<int32_t>(table), ptr(a.tensor(6)),
+                                 ptr(a.tensor(7)), ptr<float>(a.tensor(8)), ptr<float>(a.tensor(9)), ptr(o), bytes ? ptr(ws) : nullptr, bytes,
+                                 a.stream()),
+                o);
+}
+
+// sample_tokens(stream, logits, uniform, temperature, top_k, top_p, min_p, tokens, probs): (tokens, probs)
+PyObject *sample_tokens(Args &a) {
+    const Tensor &x = a.tensor(1);
+    const Tensor *u = a.maybe(2), *t = a.maybe(3), *k = a.maybe(4), *p = a.maybe(5), *m = a.maybe(6);
+    const bool draws = a.flag(7), spreads = a.flag(8);
+    need(x.dim() == 2 && x.size(1) > 0 && (u || !draws));
+    kda_sample_desc d{};
+    d.num_rows = narrow(x.size(0));
+    d.vocab = narrow(x.size(1));
+    d.logits_dtype = code(x.scalar_type());
+    d.stride = rows(x, x.scalar_type(), d.num_rows, d.vocab);
+    if (u) whole(*u, at::kFloat, d.num_rows, {});
+    if (t) whole(*t, at::kFloat, d.num_rows, {});
+    if (k) whole(*k, at::kInt, d.num_rows, {});
+    if (p) whole(*p, at::kFloat, d.num_rows, {});
+    if (m) whole(*m, at::kFloat, d.num_rows, {});
+    const Tensor tokens = draws ? fresh(x, {d.num_rows}, at::kInt) : Tensor(), probs = spreads ? fresh(x, x.sizes(), at::kFloat) : Tensor();
+    const size_t bytes = kda_sample_tokens_workspace_size(&d);
+    const Tensor ws = bytes ? fresh(x, {(int64_t)bytes}, at::kByte) : Tensor();
+    const kda_status s = kda_sample_tokens(&d, ptr(x), ptr<float>(u), ptr<float>(t), ptr<int32_t>(k), ptr<float>(p), ptr<float>(m),
+                                           draws ? ptr<int32_t>(tokens) : nullptr, spreads ? ptr<float>(probs) : nullptr,
+                                           bytes ? ptr(ws) : nullptr, bytes, a.stream());
+    if (s != KDA_OK) return PyLong_FromLong(s);
+    if (draws && spreads) return done(s, tokens, nullptr, probs);
+    return THPVariable_Wrap(draws ? tokens : probs);
+}
+
 template <PyObject *(*F)(Args &), int N> PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t count) {
     HANDLE_TH_ERRORS
     if (count != N) {
@@ -347,6 +506,12 @@ PyMethodDef methods[] = {
     {"ssm_decode_multi", fast<ssm_decode_multi, 14>(), METH_FASTCALL, nullptr},
     {"verify_drafts", fast<verify_drafts, 7>(), METH_FASTCALL, nullptr},
     {"commit_states", fast<commit_states, 5>(), METH_FASTCALL, nullptr},
+    {"kv_reserve", fast<kv_reserve, 10>(), METH_FASTCALL, nullptr},
+    {"kv_commit", fast<kv_commit, 7>(), METH_FASTCALL, nullptr},
+    {"kv_release", fast<kv_release, 9>(), METH_FASTCALL, nullptr},
+    {"kv_store", fast<kv_store, 8>(), METH_FASTCALL, nullptr},
+    {"kv_attention", fast<kv_attention, 11>(), METH_FASTCALL, nullptr},
+    {"sample_tokens", fast<sample_tokens, 9>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,581 @@
+// Causal attention over a paged cache of 8-bit keys and values.
+//
+//   o_j = sum_i p_ij v_i / sum_i p_ij,  p_ij = exp(scale q_j . k_i - m_j),  i <= last_j
+//
+// with a running reference m (softmax's value does not depend on it).  A query
+// is a column: the g query heads that share a key head, times the tokens, are
+// the columns of S^T = K Q^T and O^T = V^T P^T, so keys and values are read
+// once for all of them and both are the matrix cores' A operand.
+//
+// Fragments come straight from memory, 16 bytes a lane, without LDS: the rows
+// of a 64-key tile are numbered so that the four S^T tiles leave lane group
+// l / 16 with the scores of its keys 16 (l / 16) .. + 15, which is what the B
+// operand of the second product wants from it, and so that its share of V^T is
+// 16 consecutive tokens of one channel (values are stored with tokens side by
+// side).  Head channels are taken in the order 64 j + 16 (l / 16) + e for the
+// same reason.  e4m3 widens to bf16 exactly, and the block's power-of-two scale
+// goes in with it.
+//
+// Arithmetic: bf16 queries are operands as they are and p is rounded to bf16;
+// fp32 queries and their p go in as the sum of three bf16 terms.  Scores, sums
+// and outputs accumulate in fp32.
+//
+// Work is cut into (request, columns, chunk of keys) units over a fixed number
+// of places: the chunk length follows from the lengths on the device, such that
+// the places always suffice and hold about equal work.  Chunks of one column
+// are joined by a second launch.
+#include <algorithm>
+
+#include "kda_device.h"
+#include "kda_internal.h"
+
+namespace kda {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kTile = 64;
+constexpr float kNone = -1e30f;   // a reference below every score
+
+// How a call is laid out over the chip.  Columns of a workgroup: SPLIT kernels
+// give their four waves the same 16 NT columns and every fourth key tile,
+// the others each wave 16 NT of its own.
+struct Layout {
+    int nt;
+    bool split;
+    int cols;        // of a workgroup
+    long units;      // (request, columns) pairs, at most
+    long places;     // units and room for chunks
+};
+
+Layout layout_of(int num_seqs, int total_tokens, int q_heads, int heads, bool io_bf16) {
+    Layout y{};
+    const long g = q_heads / heads, columns = (long)total_tokens * g, each = num_seqs ? (columns + num_seqs - 1) / num_seqs : 0;
+    y.nt = each <= 16 ? 1 : each <= 32 || !io_bf16 ? 2 : 4;
+    y.split = each <= 32;
+    y.cols = 16 * y.nt * (y.split ? 1 : kWaves);
+    y.units = columns / y.cols + num_seqs;
+    long more = 0;
+    if (y.split) more = std::max<long>((1536 + heads - 1) / heads, y.units / 4);
+    else if (y.units * heads < 512) more = (1024 + heads - 1) / heads;
+    y.places = y.units + more;
+    return y;
+}
+
+struct Plan {
+    int units, places, least;   // least: tiles of a chunk
+    int *info;                  // [0]: chunk length; then first place and chunks of every request
+    float *sums;                // [places, heads, cols, 2]: m, l
+    float *parts;               // [places, heads, cols, d]
+};
+
+size_t info_bytes(int num_seqs) { return ((size_t)num_seqs * 8 + 16 + 255) / 256 * 256; }
+
+__device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
+    return x;
+}
+__device__ __forceinline__ unsigned long long wave_sum(unsigned long long x) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
+    return x;
+}
+
+struct Request { int begin, length, total, units, tiles; };
+
+__device__ __forceinline__ Request request_of(const AttendArgs &a, int n, int g, int cols) {
+    Request r;
+    r.begin = max(a.cu_seqlens[n], 0);
+    r.length = max(min(a.cu_seqlens[n + 1], a.total_tokens) - r.begin, 0);
+    const int row = a.indices[n];
+    const long most = (long)a.max_blocks << a.block_shift;
+    r.total = (unsigned)row < (unsigned)a.rows ? (int)min((long)max(a.kv_totals[n], 0), most) : 0;
+    r.units = (int)(((long)r.length * g + cols - 1) / cols);
+    r.tiles = (int)(((long)r.total + kTile - 1) / kTile);
+    return r;
+}
+
+struct Unit { int n, column, chunk, chunks, length; };   // column: index of the unit's columns; length: tiles of a chunk
+
+// What place p stands for (n < 0: nothing).  Every workgroup finds it by itself
+// from the lengths, which takes a microsecond for some hundred requests; a
+// launch before this one would take four.
+__device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int cols, bool tell) {
+    __shared__ unsigned long long work[kWaves];
+    __shared__ uint32_t part[kWaves];
+    __shared__ int found[4];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    Unit u{-1, 0, 0, 1, INT32_MAX / 2};
+    if (plan.places > plan.units) {
+        unsigned long long w = 0;
+        for (int n = tid; n < a.num_seqs; n += kThreads) {
+            const Request r = request_of(a, n, g, cols);
+            w += (unsigned long long)r.units * r.tiles;
+        }
+        w = wave_sum(w);
+        if (lane == 0) work[wave] = w;
+        __syncthreads();
+        w = work[0] + work[1] + work[2] + work[3];
+        const unsigned long long room = plan.places - plan.units;
+        u.length = (int)max((unsigned long long)plan.least, (w + room - 1) / room);
+    }
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int n0 = 0; n0 < a.num_seqs; n0 += kThreads) {
+        const int n = n0 + tid;
+        uint32_t take = 0;
+        int chunks = 1;
+        if (n < a.num_seqs) {
+            const Request r = request_of(a, n, g, cols);
+            chunks = max(1, (r.tiles + u.length - 1) / u.length);
+            take = (uint32_t)r.units * chunks;
+        }
+        uint32_t incl = take;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const uint32_t y = __shfl_up(incl, m, 64);
+            if (lane >= m) incl += y;
+        }
+        if (lane == 63) part[wave] = incl;
+        __syncthreads();
+        uint32_t all = 0;
+        incl += before;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) incl += part[w];
+            all += part[w];
+        }
+        if (tell && n < a.num_seqs) {
+            plan.info[4 + 2 * n] = (int)(incl - take);
+            plan.info[5 + 2 * n] = chunks;
+        }
+        if ((uint32_t)p < incl && (uint32_t)p >= incl - take) {
+            found[0] = n;
+            found[1] = (int)(p - (incl - take)) / chunks;
+            found[2] = (int)(p - (incl - take)) % chunks;
+            found[3] = chunks;
+        }
+        before += all;
+        __syncthreads();
+        if (!tell && before > (uint32_t)p) break;
+    }
+    if (tell && tid == 0) plan.info[0] = u.length;
+    u.n = found[0];
+    u.column = found[1];
+    u.chunk = found[2];
+    u.chunks = found[3];
+    return u;
+}
+
+// x as the sum of TERMS bf16 values.
+template <int TERMS> __device__ __forceinline__ void terms_of(float x, int e, bf16x8 (&t)[TERMS]) {
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+        const __bf16 y = (__bf16)x;
+        t[i][e] = y;
+        if (i + 1 < TERMS) x -= (float)y;
+    }
+}
+
+// Eight e4m3 values (two words) as bf16, times a power of two.
+__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi, float scale) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+
+// Bytes of w that are NaN, as 0x80 in each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+template <typename T, int D, int NT, bool SPLIT>
+__global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const AttendArgs a, const Plan plan) {
+    constexpr int TERMS = sizeof(T) == 4 ? 3 : 1, KL = D / 64, MT = D / 16, WAVE = 16 * NT, COLS = SPLIT ? WAVE : kWaves * WAVE;
+    __shared__ float joined[kWaves][4][256];
+    __shared__ float stats[kWaves][WAVE][2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, grp = lane >> 4;
+    const int head = blockIdx.x % a.heads, place = blockIdx.x / a.heads, g = a.q_heads / a.heads;
+    const Unit u = unit_of(a, plan, place, g, COLS, place == 0 && head == 0 && plan.places > plan.units);
+    if (u.n < 0) return;
+    const Request r = request_of(a, u.n, g, COLS);
+    // the last columns first: they see the most keys
+    const int all = r.length * g, first = (r.units - 1 - u.column) * COLS, end = min(first + COLS, all);
+    const int before = r.total - r.length;                                // position of the request's first token
+    const int unit_keys = max(before + (end - 1) / g + 1, 0);
+    const int unit_tiles = (unit_keys + kTile - 1) / kTile;
+    const int chunks = max(1, (unit_tiles + u.length - 1) / u.length);    // that this unit really has
+    if (u.chunk >= chunks) return;
+    const bool same = SPLIT || end - first <= WAVE;                       // the waves share columns and split the keys
+    const int col0 = first + (same ? 0 : wave * WAVE), col1 = min(col0 + WAVE, end);
+    const int seen = col1 > col0 ? max(before + (col1 - 1) / g + 1, 0) : 0;   // keys that some column of this wave sees
+    const int least = col1 > col0 ? before + col0 / g : -1;                   // the last key that all of them see
+    const int step = same ? kWaves : 1;
+    const int stop = min((u.chunk + 1) * u.length, (seen + kTile - 1) / kTile);
+    int tile = u.chunk * u.length + (same ? wave : 0);
+
+    // queries
+    bf16x8 q[NT][KL][2][TERMS];
+    int last[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int col = col0 + 16 * nt + c;
+        const bool in = col < col1;
+        const int token = in ? col / g : 0, h = in ? col - token * g : 0;
+        last[nt] = in ? before + token : -1;
+        const T *src = static_cast<const T *>(a.q) + (long)(r.begin + token) * a.q_stride + ((long)head * g + h) * D;
+#pragma unroll
+        for (int j = 0; j < KL; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const T *at = src + 64 * j + 16 * grp + 8 * s;
+                if constexpr (TERMS == 1) {
+                    u32x4 w{0, 0, 0, 0};
+                    if (in) w = *reinterpret_cast<const u32x4 *>(at);
+                    q[nt][j][s][0] = __builtin_bit_cast(bf16x8, w);
+                } else {
+                    f32x4 x{0.f, 0.f, 0.f, 0.f}, y{0.f, 0.f, 0.f, 0.f};
+                    if (in) {
+                        x = load4(at);
+                        y = load4(at + 4);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        terms_of<TERMS>(x[e], e, q[nt][j][s]);
+                        terms_of<TERMS>(y[e], 4 + e, q[nt][j][s]);
+                    }
+                }
+            }
+    }
+
+    const int bs = 1 << a.block_shift, within = bs - 1;
+    const int32_t *table = a.block_table + (long)a.indices[u.n] * a.max_blocks;
+    const float to2 = a.scale * kLog2e;
+    const auto page = [&](int tile, int group) {
+        const int i = (tile * kTile + 16 * group) >> a.block_shift;
+        return table[min(i, a.max_blocks - 1)];
+    };
+    u32x4 kr[4][KL], vr[MT];
+    float ks, vs;
+    bool fine;   // this lane's sixteen keys begin in a block that holds some
+    const auto load_k = [&](int tile, int block) {
+        const int b = (unsigned)block < (unsigned)a.num_blocks ? block : 0, off = (tile * kTile + 16 * (c >> 2)) & within;
+        const long at = (long)b * a.heads + head;
+        ks = a.k_scale[at];
+        const uint8_t *p = a.k_cache + (at * bs + off + (c & 3)) * D + 16 * grp;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < KL; ++j) kr[t][j] = *reinterpret_cast<const u32x4 *>(p + 4 * t * D + 64 * j);
+    };
+    const auto load_v = [&](int tile, int block) {
+        fine = (unsigned)block < (unsigned)a.num_blocks && tile * kTile + 16 * grp < r.total;
+        const int b = fine ? block : 0, off = (tile * kTile + 16 * grp) & within;
+        const long at = (long)b * a.heads + head;
+        vs = fine ? a.v_scale[at] : 1.f;
+        const uint8_t *p = a.v_cache + (at * D + c) * bs + off;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) vr[t] = *reinterpret_cast<const u32x4 *>(p + 16 * t * bs);
+    };
+
+    f32x4 o[MT][NT];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt] = kNone;
+        l[nt] = 0.f;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) o[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    if (tile < stop) {
+        load_k(tile, page(tile, c >> 2));
+        load_v(tile, page(tile, grp));
+    }
+    for (; tile < stop; tile += step) {
+        const int next = min(tile + step, stop - 1);   // the last one is loaded again, unused
+        const int kpage = page(next, c >> 2), vpage = page(next, grp);
+        f32x4 s[4][NT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < KL; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bf16x8 k = widen(kr[t][j][2 * h], kr[t][j][2 * h + 1], ks);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = TERMS - 1; i >= 0; --i) s[t][nt] = mma(k, q[nt][j][h][i], s[t][nt]);
+                }
+        load_k(next, kpage);
+        const bool masked = tile * kTile + kTile - 1 > least || __any(!fine);
+        if (masked) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!fine || tile * kTile + 16 * grp + 4 * t + i > last[nt]) s[t][nt][i] = -__builtin_inff();
+        }
+        // a reference that holds until a score passes it by 2^8
+        float top[NT];
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float x = s[0][nt][0];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x = __builtin_fmaxf(x, s[t][nt][i]);
+            x = __builtin_fmaxf(x, __shfl_xor(x, 16, 64));
+            x = __builtin_fmaxf(x, __shfl_xor(x, 32, 64));
+            top[nt] = x;
+            raise |= (x - m[nt]) * to2 > 8.f;
+        }
+        if (__any(raise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float to = __builtin_fmaxf(m[nt], top[nt]), f = __builtin_amdgcn_exp2f((m[nt] - to) * to2);
+                m[nt] = to;
+                l[nt] *= f;
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[t][nt][i] *= f;
+            }
+        }
+        bf16x8 p[NT][2][TERMS];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float shift = -m[nt] * to2;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][nt][i], to2, shift));
+                    l[nt] += x;
+                    terms_of<TERMS>(x, 4 * (t & 1) + i, p[nt][t >> 1]);
+                }
+        }
+        if (masked) {
+            // what a column must not see may be NaN, and 0 * NaN would reach it
+            uint32_t bad = 0;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bad |= nan_bytes(vr[t][i]);
+            if (__any(bad != 0)) {
+                bf16x8 one[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            one[nt][h][e] = (__bf16)(!fine || tile * kTile + 16 * grp + 8 * h + e > last[nt] ? 0.f : 1.f);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    f32x4 hit[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) hit[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    u32x4 flag;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t b = nan_bytes(vr[t][i]) >> 7;
+                        vr[t][i] &= ~(b * 0xffu);
+                        flag[i] = b * 0x38u;   // e4m3's one
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bf16x8 f = widen(flag[2 * h], flag[2 * h + 1], 1.f);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) hit[nt] = mma(f, one[nt][h], hit[nt]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (hit[nt][i] > 0.f) o[t][nt][i] = __builtin_nanf("");
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bf16x8 v = widen(vr[t][2 * h], vr[t][2 * h + 1], vs);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = TERMS - 1; i >= 0; --i) o[t][nt] = mma(v, p[nt][h][i], o[t][nt]);
+            }
+        load_v(next, vpage);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        l[nt] += __shfl_xor(l[nt], 16, 64);
+        l[nt] += __shfl_xor(l[nt], 32, 64);
+    }
+
+    const bool alone = chunks == 1;
+    const long at = (long)place * a.heads + head;
+    // channels 16 t + 4 grp .. + 3 of column c of tile nt
+    const auto write = [&](int t, int nt, int col, f32x4 x, float sum) {
+        if (col >= end) return;
+        const int d = 16 * t + 4 * grp;
+        if (alone) {
+            const int token = col / g, h = col - token * g;
+            T *to = static_cast<T *>(a.o) + ((long)(r.begin + token) * a.q_heads + (long)head * g + h) * D + d;
+            const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] *= f;
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<f32x4 *>(to) = x;
+            else *reinterpret_cast<u32x2 *>(to) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+        } else {
+            *reinterpret_cast<f32x4 *>(plan.parts + (at * COLS + col - first) * D + d) = x;
+        }
+    };
+    if (!same) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = col0 + 16 * nt + c;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) write(t, nt, col, o[t][nt], l[nt]);
+            if (!alone && grp == 0 && col < end) *reinterpret_cast<f32x2 *>(plan.sums + (at * COLS + col - first) * 2) = f32x2{m[nt], l[nt]};
+        }
+        return;
+    }
+    // the waves' sums come together
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        if (grp == 0) {
+            stats[wave][16 * nt + c][0] = m[nt];
+            stats[wave][16 * nt + c][1] = l[nt];
+        }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float to = kNone, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) to = __builtin_fmaxf(to, stats[w][16 * nt + c][0]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sum += stats[w][16 * nt + c][1] * __builtin_amdgcn_exp2f((stats[w][16 * nt + c][0] - to) * to2);
+        const float f = __builtin_amdgcn_exp2f((m[nt] - to) * to2);
+        const int col = col0 + 16 * nt + c;
+#pragma unroll
+        for (int t0 = 0; t0 < MT; t0 += 4) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f32x4 x = o[t0 + t][nt];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] *= f;
+                *reinterpret_cast<f32x4 *>(&joined[wave][t][4 * lane]) = x;
+            }
+            __syncthreads();
+            f32x4 x = *reinterpret_cast<const f32x4 *>(&joined[0][wave][4 * lane]);
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) x += *reinterpret_cast<const f32x4 *>(&joined[w][wave][4 * lane]);
+            write(t0 + wave, nt, col, x, sum);
+            __syncthreads();
+        }
+        if (!alone && wave == 0 && grp == 0 && col < end) *reinterpret_cast<f32x2 *>(plan.sums + (at * COLS + col - first) * 2) = f32x2{to, sum};
+    }
+}
+
+// The chunks of a column (token, query head) joined; one wave a column.
+template <typename T, int D> __global__ __launch_bounds__(256) void join_kernel(const AttendArgs a, const Plan plan, int cols) {
+    const int lane = threadIdx.x & 63, g = a.q_heads / a.heads;
+    const long column = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int token = (int)(column / a.q_heads), qh = (int)(column % a.q_heads), head = qh / g;
+    if (token >= a.total_tokens) return;
+    int lo = 0, num = a.num_seqs;
+    while (num > 1) {
+        const int half = num >> 1;
+        if (a.cu_seqlens[lo + half] <= token) {
+            lo += half;
+            num -= half;
+        } else {
+            num = half;
+        }
+    }
+    const Request r = request_of(a, lo, g, cols);
+    if (token < r.begin || token - r.begin >= r.length) return;
+    const int col = (token - r.begin) * g + (qh - head * g), ct = col / cols, length = plan.info[0];
+    const int end = min((ct + 1) * cols, r.length * g);
+    const int keys = max(r.total - r.length + (end - 1) / g + 1, 0), tiles = (keys + kTile - 1) / kTile;
+    const int chunks = max(1, (tiles + length - 1) / length);
+    if (chunks == 1) return;
+    const long place = plan.info[4 + 2 * lo] + (long)(r.units - 1 - ct) * plan.info[5 + 2 * lo];
+    if (place + chunks > plan.places) return;   // offsets that do not fit the call
+    const float to2 = a.scale * kLog2e;
+    const auto at = [&](int k) { return ((place + k) * a.heads + head) * cols + col - ct * cols; };
+    float top = kNone;
+    for (int k = 0; k < chunks; ++k) top = __builtin_fmaxf(top, plan.sums[at(k) * 2]);
+    float sum = 0.f, x[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) x[i] = 0.f;
+    for (int k = 0; k < chunks; ++k) {
+        const f32x2 ml = *reinterpret_cast<const f32x2 *>(plan.sums + at(k) * 2);
+        const float f = __builtin_amdgcn_exp2f((ml[0] - top) * to2);
+        sum += f * ml[1];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) x[i] += f * plan.parts[at(k) * D + lane + 64 * i];
+    }
+    T *to = static_cast<T *>(a.o) + column * D;
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) io_traits<T>::store(to, lane + 64 * i, x[i] * f);
+}
+
+template <typename T, int D, int NT, bool SPLIT>
+hipError_t launch(const AttendArgs &a, const Layout &y, const Plan &plan, hipStream_t stream) {
+    attend_kernel<T, D, NT, SPLIT><<<(unsigned)(plan.places * a.heads), kThreads, 0, stream>>>(a, plan);
+    if (plan.places > plan.units) {
+        const long columns = (long)a.total_tokens * a.q_heads;
+        join_kernel<T, D><<<(unsigned)((columns + 3) / 4), 256, 0, stream>>>(a, plan, y.cols);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int D> hipError_t launch(const AttendArgs &a, const Layout &y, const Plan &plan, hipStream_t stream) {
+    if (y.split) return y.nt == 1 ? launch<T, D, 1, true>(a, y, plan, stream) : launch<T, D, 2, true>(a, y, plan, stream);
+    if constexpr (sizeof(T) == 4) return launch<T, D, 2, false>(a, y, plan, stream);
+    else return launch<T, D, 4, false>(a, y, plan, stream);
+}
+
+}  // namespace
+
+size_t attend_workspace_bytes(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16) {
+    const Layout y = layout_of(num_seqs, total_tokens, q_heads, heads, io_bf16);
+    if (y.places == y.units) return 0;
+    return info_bytes(num_seqs) + (size_t)y.places * heads * y.cols * (d + 2) * sizeof(float);
+}
+
+long attend_grid(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16) {
+    const Layout y = layout_of(num_seqs, total_tokens, q_heads, heads, io_bf16);
+    return std::max(y.places * heads, ((long)total_tokens * q_heads + 3) / 4);
+}
+
+hipError_t launch_attend(const AttendArgs &a, void *workspace, hipStream_t stream) {
+    const Layout y = layout_of(a.num_seqs, a.total_tokens, a.q_heads, a.heads, a.io_bf16);
+    Plan plan{};
+    plan.units = (int)y.units;
+    plan.places = (int)y.places;
+    plan.least = y.split ? kWaves : 8;
+    plan.info = static_cast<int *>(workspace);
+    plan.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + info_bytes(a.num_seqs));
+    plan.sums = plan.parts + (size_t)y.places * a.heads * y.cols * a.d;
+    if (a.io_bf16) return a.d == 64 ? launch<bf16, 64>(a, y, plan, stream) : launch<bf16, 128>(a, y, plan, stream);
+    return a.d == 64 ? launch<float, 64>(a, y, plan, stream) : launch<float, 128>(a, y, plan, stream);
+}
+
+}  // namespace kda

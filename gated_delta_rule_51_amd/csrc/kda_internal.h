@@ -111,4 +111,57 @@ hipError_t launch_verify(const VerifyArgs &a, hipStream_t stream);
 hipError_t launch_commit(const int32_t *indices, const int32_t *steps, const void *cache, void *pool, int num_seqs,
                          int num_slots, int cache_steps, int cache_pitch, long row_bytes, hipStream_t stream);
 
+// Block tables and slot maps of the paged cache.
+struct PagesArgs {
+    const int32_t *cu_seqlens, *indices, *steps, *keep_lens;   // steps, keep_lens: or NULL
+    int32_t *kv_lens, *blocks_held, *block_table, *free_blocks, *free_count;
+    int32_t *slots, *kv_totals;
+    int num_seqs, total_tokens, rows, max_blocks, block_shift, num_free;
+};
+hipError_t launch_reserve(const PagesArgs &a, hipStream_t stream);
+hipError_t launch_release(const PagesArgs &a, hipStream_t stream);
+hipError_t launch_kv_commit(const PagesArgs &a, hipStream_t stream);
+
+// Keys and values into their blocks in 8 bits.
+struct StoreArgs {
+    const void *k, *v;
+    const int32_t *slots;
+    uint8_t *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    int total_tokens, heads, d, block_shift, num_blocks;
+    bool io_bf16;
+    long k_stride, v_stride;
+};
+hipError_t launch_kv_store(const StoreArgs &a, hipStream_t stream);
+
+// Attention over the blocks.
+struct AttendArgs {
+    const void *q;
+    const int32_t *cu_seqlens, *kv_totals, *indices, *block_table;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    void *o;
+    int num_seqs, total_tokens, q_heads, heads, d, block_shift, num_blocks, rows, max_blocks;
+    bool io_bf16;
+    long q_stride;
+    float scale;
+};
+size_t attend_workspace_bytes(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16);
+long attend_grid(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16);   // workgroups of the launch
+hipError_t launch_attend(const AttendArgs &a, void *workspace, hipStream_t stream);
+
+// The next token and the probabilities it is drawn from.
+struct SampleArgs {
+    const void *logits;
+    const float *uniform, *temperature, *top_p, *min_p;   // the last three, top_k, tokens and probs: or NULL
+    const int32_t *top_k;
+    int32_t *tokens;
+    float *probs;
+    int rows, vocab;
+    bool bf16;
+    long stride;
+};
+size_t sample_workspace_bytes(int rows, int vocab, bool bf16);
+hipError_t launch_sample(const SampleArgs &a, void *workspace, hipStream_t stream);
+
 }  // namespace kda

@@ -5,7 +5,9 @@
  * either densely or in place in a state pool.  Beside them the steps a serving
  * path needs next to them: the short causal convolution, the selective
  * state-space scan on the same pools, and the verification of drafted tokens
- * with the commit of the accepted states.
+ * with the commit of the accepted states; and what the layers of attention
+ * between the recurrent ones need: a paged cache of 8-bit keys and values and the
+ * attention over it, and the choice of the next token.
  *
  * The operation (per sequence and value head; S is the K x V state):
  *     S'  = Diag(exp g_t) S          decay, one factor per key channel
@@ -542,6 +544,178 @@ typedef struct {
 kda_status kda_commit_states(const kda_commit_desc *desc, void *state_pool,
                              const int32_t *state_indices, const void *intermediate_states,
                              const int32_t *steps, void *stream);
+
+/* ---- Paged cache: blocks, slots, 8-bit keys and values, attention --------- */
+
+/*
+ * The layers of attention between recurrent ones keep every token's keys and
+ * values, in blocks of block_size tokens (16, 32, 64 or 128) of one cache:
+ *   k_cache [num_blocks, Hk, block_size, D], v_cache [num_blocks, Hk, D,
+ *   block_size]: 8-bit floats (OCP e4m3: 4 exponent and 3 fraction bits, largest
+ *   448, no infinity), tokens of a value channel side by side;
+ *   k_scale, v_scale [num_blocks, Hk] fp32, powers of two: a stored value times
+ *   its block's scale is the number it stands for.
+ * A request has a row of the block table, as it has a row of the state pools:
+ * state_indices [N] names the rows of kv_lens, blocks_held [rows] (tokens in the
+ * cache; blocks in the table) and block_table [rows, max_blocks] (block ids).
+ * Unlike in the pools no row is a sentinel: a request with an index outside
+ * [0, rows) is padding, takes no blocks, has nothing in the cache and its
+ * queries see nothing.  Rows of real requests are unique (not checked).
+ * free_blocks [num_free] is a stack of the ids of free blocks, free_count [1] how
+ * many of them there are.  A slot is block * block_size + offset, below 2^31.
+ * In these calls arrays of 32-bit words need an alignment of 4 bytes only.
+ */
+typedef struct {
+    int32_t num_seqs;     /* N >= 0 requests                                       */
+    int32_t total_tokens; /* T >= 0 rows of the slot map, >= cu_seqlens[N]          */
+    int32_t rows;         /* rows of the table                                     */
+    int32_t max_blocks;   /* entries of a row; max_blocks * block_size <= 2^30      */
+    int32_t block_size;   /* 16, 32, 64 or 128                                     */
+    int32_t num_free;     /* length of free_blocks                                 */
+} kda_pages_desc;
+
+/*
+ * Blocks and slots for the tokens to come.  Request n holds kv_lens[row] tokens
+ * and brings cu_seqlens[n + 1] - cu_seqlens[n] more; the blocks it lacks for them
+ * are taken from the top of free_blocks, in the batch's order, and entered in its
+ * row.  From the first request on whose blocks are no longer there, none takes
+ * any; one whose row is too short takes none and does not count.
+ *   slots     [T] int32: every token's slot, -1 for those of a request that did
+ *             not get its blocks or is padding, and past cu_seqlens[N]
+ *   kv_totals [N] int32: tokens held and new, 0 for such a request
+ * blocks_held, block_table, free_count are updated; kv_lens is not: kda_kv_commit
+ * counts the tokens once they stand.  A second call for the same tokens takes
+ * nothing more and gives the same slots.
+ */
+kda_status kda_kv_reserve(const kda_pages_desc *desc, const int32_t *cu_seqlens,
+                          const int32_t *state_indices, const int32_t *kv_lens,
+                          int32_t *blocks_held, int32_t *block_table, const int32_t *free_blocks,
+                          int32_t *free_count, int32_t *slots, int32_t *kv_totals, void *stream);
+
+/*
+ * kv_lens[row] grows by the request's tokens, or with steps [N] (as for
+ * kda_commit_states: the accepted step of a run of drafts) by steps[n] + 1; a step
+ * that is negative or not below the request's length, or a length beyond the
+ * request's blocks, leaves it as it is.  Blocks of tokens that did not stand stay
+ * with the request.  total_tokens, max_blocks and num_free play no part.
+ */
+kda_status kda_kv_commit(const kda_pages_desc *desc, const int32_t *cu_seqlens,
+                         const int32_t *steps, const int32_t *state_indices, int32_t *kv_lens,
+                         const int32_t *blocks_held, void *stream);
+
+/*
+ * Requests give blocks back: kv_lens[row] becomes min(kv_lens[row], keep_lens[n])
+ * (0 with keep_lens NULL: the request ends), and the blocks its tokens do not
+ * reach go to the top of free_blocks, such that releasing what the last
+ * kda_kv_reserve of the same batch took restores the list.  Blocks that the list
+ * has no room for are dropped.  A block that several rows name must not be
+ * released while one of them uses it (not checked).  total_tokens plays no part.
+ */
+kda_status kda_kv_release(const kda_pages_desc *desc, const int32_t *keep_lens,
+                          const int32_t *state_indices, int32_t *kv_lens, int32_t *blocks_held,
+                          const int32_t *block_table, int32_t *free_blocks, int32_t *free_count,
+                          void *stream);
+
+typedef struct {
+    int32_t num_seqs;     /* kda_kv_attention: N >= 0 requests                     */
+    int32_t total_tokens; /* T >= 0                                                */
+    int32_t q_heads;      /* kda_kv_attention: Hq, Hq % Hk == 0                    */
+    int32_t kv_heads;     /* Hk                                                    */
+    int32_t head_dim;     /* D in {64, 128}                                        */
+    int32_t block_size;   /* 16, 32, 64 or 128                                     */
+    int32_t num_blocks;   /* blocks of the caches, num_blocks * block_size < 2^31   */
+    int32_t rows, max_blocks; /* kda_kv_attention: of the block table               */
+    int32_t io_dtype;     /* kda_dtype of q, k, v and o                            */
+    float scale;          /* kda_kv_attention: of the scores, 0 < scale <= 2^20     */
+    int64_t q_stride, k_stride, v_stride; /* elements between two token rows        */
+} kda_kv_desc;
+
+/*
+ * Keys and values into the cache.  Token t goes to slots[t] (a slot outside the
+ * cache: nowhere).  Consecutive tokens on consecutive slots of a block are a run;
+ * a block takes one run in a call (not checked), and holds already what lies
+ * before the run.  With a the largest |x| of the run and head, a scale 2^e with
+ * the least e >= -100 for which a <= 448 * 2^e is needed; the block's scale becomes
+ * that, or, where the block holds tokens, the larger of the two, and those tokens
+ * are then stored again under it (exact but below e4m3's least normal number).
+ * Values are rounded to the nearest, ties to even.  Infinities and NaN are stored
+ * as NaN and play no part in a.  Bytes behind the run stay as they were.
+ *   k, v  [T, Hk, D] io dtype, token rows k_stride and v_stride elements apart (a
+ *         multiple of 16 bytes), contiguous within a row
+ *   slots [T] int32
+ */
+kda_status kda_kv_store(const kda_kv_desc *desc, const void *k, const void *v, const int32_t *slots,
+                        void *k_cache, void *v_cache, float *k_scale, float *v_scale, void *stream);
+
+/*
+ * Causal attention of every request's new tokens over all of its tokens in the
+ * cache, its own among them (kda_kv_store comes first).  Token j of L of request
+ * n stands at position kv_totals[n] - L + j and sees the positions up to it:
+ *     o = sum_i softmax_i(scale q . k_i) v_i
+ * query head h over key head h / (Hq / Hk).  A token that sees nothing gives
+ * zeros.  One token a request, runs of drafts and prompts, in any mixture.
+ *   q          [T, Hq, D] io dtype, token rows q_stride elements apart (a multiple
+ *              of 16 bytes)
+ *   kv_totals  [N] int32; more than the row's blocks hold counts as that
+ *   block_table, state_indices: as above; an entry outside [0, num_blocks) holds
+ *              nothing, and the tokens it would hold are not seen
+ *   o          [T, Hq, D] io dtype, contiguous; rows past cu_seqlens[N] are not
+ *              written; must not overlap any input
+ * Precision: keys and values are exact in bf16, the matrix cores' operands.  bf16
+ * queries are operands as they are, and softmax's numerators are rounded to bf16
+ * (2^-8 of each) for the second product; with fp32 io queries and numerators go
+ * in as the sum of three bf16 terms, which hold all their bits.  Scores, sums and
+ * outputs accumulate in fp32.  What a token does not see has no part in its
+ * output, NaN or not.
+ * The workspace overlaps nothing else; it may be reused by calls that are ordered
+ * on one stream.  T * Hq < 2^31.
+ */
+size_t kda_kv_attention_workspace_size(const kda_kv_desc *desc);
+kda_status kda_kv_attention(const kda_kv_desc *desc, const void *q, const int32_t *cu_seqlens,
+                            const int32_t *kv_totals, const int32_t *state_indices,
+                            const int32_t *block_table, const void *k_cache, const void *v_cache,
+                            const float *k_scale, const float *v_scale, void *o, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* ---- The next token ------------------------------------------------------- */
+
+typedef struct {
+    int32_t num_rows;     /* N >= 0                                                */
+    int32_t vocab;        /* 0 < V <= 2^20                                         */
+    int32_t logits_dtype; /* kda_dtype                                             */
+    int64_t stride;       /* elements between two rows of logits, >= V             */
+} kda_sample_desc;
+
+/*
+ * The next token of every row of logits [N, V], and the probabilities it is drawn
+ * from.  With w_i = exp((x_i - max x) / temperature), in the order of falling
+ * logits, equal ones by rising index:
+ *   top_k      keeps the first top_k (0 or less, or V and more: all)
+ *   top_p      of those, the shortest beginning whose weights' sum is at least
+ *              top_p times theirs, at least one (1 and more: all)
+ *   min_p      of those, w >= min_p (0 or less: all; above 1 counts as 1)
+ * and the token is the first index i, in the order of indices, with
+ * cum_i > uniform * cum_{V-1}, cum the running sums of the weights kept.  A
+ * temperature that is not above 0 takes the largest logit, the lowest index of
+ * equal ones.  Every limit has an entry a row:
+ *   temperature, top_p, min_p [N] fp32, top_k [N] int32: each may be NULL (1, all)
+ *   uniform     [N] fp32 in [0, 1); tokens [N] int32; both NULL for probabilities
+ *               alone
+ *   probs       [N, V] fp32, contiguous, or NULL: w over the sum of those kept, 0
+ *               for the others: the distributions that kda_verify_drafts takes
+ * A NaN logit is none.  A row without any logit above minus infinity gives -1 and
+ * zeros; where the largest is infinite, those that equal it share all weight.
+ * Weights are formed in fp64 and summed as multiples of 2^-46 (2^-45 over 65,536
+ * tokens, and so on), so that a token and its cut are the same from call to call
+ * and those of exact sums but where a border lies within that rounding.  Outputs
+ * overlap no input and not one another.  The workspace may be reused by calls that
+ * are ordered on one stream; it may be NULL where its size is 0.
+ */
+size_t kda_sample_tokens_workspace_size(const kda_sample_desc *desc);
+kda_status kda_sample_tokens(const kda_sample_desc *desc, const void *logits, const float *uniform,
+                             const float *temperature, const int32_t *top_k, const float *top_p,
+                             const float *min_p, int32_t *tokens, float *probs, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /* Static description of a status code. */
 const char *kda_status_string(kda_status status);
