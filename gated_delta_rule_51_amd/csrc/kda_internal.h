@@ -161,7 +161,7 @@ struct SampleArgs {
     bool bf16;
     long stride;
 };
-size_t sample_workspace_bytes(int rows, int vocab, bool bf16);
+size_t sample_workspace_bytes(int rows, int vocab);
 hipError_t launch_sample(const SampleArgs &a, void *workspace, hipStream_t stream);
 
 }  // namespace kda

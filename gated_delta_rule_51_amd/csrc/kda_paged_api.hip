@@ -225,7 +225,7 @@ kda_status kda_kv_attention(const kda_kv_desc *d, const void *q, const int32_t *
 
 size_t kda_sample_tokens_workspace_size(const kda_sample_desc *d) {
     if (check_sample(d) != KDA_OK || d->num_rows == 0) return 0;
-    return sample_workspace_bytes(d->num_rows, d->vocab, d->logits_dtype == KDA_BF16);
+    return sample_workspace_bytes(d->num_rows, d->vocab);
 }
 
 kda_status kda_sample_tokens(const kda_sample_desc *d, const void *logits, const float *uniform, const float *temperature,
