@@ -518,17 +518,27 @@ template <typename T, int D> __global__ __launch_bounds__(256) void join_kernel(
     if (place + chunks > plan.places) return;   // offsets that do not fit the call
     const float to2 = a.scale * kLog2e;
     const auto at = [&](int k) { return ((place + k) * a.heads + head) * cols + col - ct * cols; };
-    float top = kNone;
-    for (int k = 0; k < chunks; ++k) top = __builtin_fmaxf(top, plan.sums[at(k) * 2]);
-    float sum = 0.f, x[D / 64];
+    float top = kNone, sum = 0.f, x[D / 64];
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) x[i] = 0.f;
-    for (int k = 0; k < chunks; ++k) {
-        const f32x2 ml = *reinterpret_cast<const f32x2 *>(plan.sums + at(k) * 2);
-        const float f = __builtin_amdgcn_exp2f((ml[0] - top) * to2);
-        sum += f * ml[1];
+    for (int k0 = 0; k0 < chunks; k0 += 64) {   // a chunk a lane
+        const int some = min(chunks - k0, 64);
+        f32x2 ml{kNone, 0.f};
+        if (lane < some) ml = *reinterpret_cast<const f32x2 *>(plan.sums + at(k0 + lane) * 2);
+        float m = ml[0];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) x[i] += f * plan.parts[at(k) * D + lane + 64 * i];
+        for (int d = 32; d >= 1; d >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d, 64));
+        const float next = __builtin_fmaxf(top, m), f = __builtin_amdgcn_exp2f((ml[0] - next) * to2), again = __builtin_amdgcn_exp2f((top - next) * to2);
+        top = next;
+        sum = sum * again + group_sum<64>(f * ml[1]);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) x[i] *= again;
+#pragma unroll 8
+        for (int k = 0; k < some; ++k) {
+            const float g = __shfl(f, k, 64);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) x[i] += g * plan.parts[at(k0 + k) * D + lane + 64 * i];
+        }
     }
     T *to = static_cast<T *>(a.o) + column * D;
     const float f = sum == 0.f ? 0.f : 1.f / sum;

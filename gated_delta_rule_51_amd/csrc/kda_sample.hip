@@ -40,20 +40,27 @@ __device__ __forceinline__ float value(const float *p, long i) { return p[i]; }
 __device__ __forceinline__ float value(const bf16 *p, long i) { return bf16_to_f32(p[i].bits); }
 
 // f(x, i) for the elements [lo, hi) of a row that starts anywhere, by THREADS
-// threads, 16 bytes a load.
-template <int THREADS, typename T, typename F> __device__ __forceinline__ void each_of(const T *x, int lo, int hi, F f) {
+// threads, 16 bytes a load, AHEAD loads at a time: a row's few workgroups wait
+// for memory otherwise.
+template <int THREADS, int AHEAD, typename T, typename F> __device__ __forceinline__ void each_of(const T *x, int lo, int hi, F f) {
     constexpr int N = 16 / (int)sizeof(T);
     const int tid = threadIdx.x, head = min(hi - lo, (int)((0 - reinterpret_cast<uintptr_t>(x + lo)) % 16 / sizeof(T)));
     if (tid < head) f(value(x, lo + tid), lo + tid);
     const int from = lo + head, wide = (hi - from) / N;
-    for (int v = tid; v < wide; v += THREADS) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(x + from + (long)v * N);
+    for (int v = tid; v < wide; v += AHEAD * THREADS) {
+        u32x4 w[AHEAD];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            float y;
-            if constexpr (N == 4) y = __uint_as_float(w[e]);
-            else y = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-            f(y, from + v * N + e);
+        for (int k = 0; k < AHEAD; ++k) w[k] = *reinterpret_cast<const u32x4 *>(x + from + (long)min(v + k * THREADS, wide - 1) * N);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (v + k * THREADS >= wide) break;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float y;
+                if constexpr (N == 4) y = __uint_as_float(w[k][e]);
+                else y = __uint_as_float(e & 1 ? w[k][e / 2] & 0xffff0000u : w[k][e / 2] << 16);
+                f(y, from + (v + k * THREADS) * N + e);
+            }
         }
     }
     const int tail = from + wide * N;
@@ -104,9 +111,26 @@ __device__ __forceinline__ Row row_at(float top, float temperature, int bits, co
     return r;
 }
 
-// 2^(j / 64)
+// 2^(j / 64), correctly rounded.
+__constant__ const double kRoots[64] = {
+    0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
+    0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
+    0x1.172b83c7d517bp+0, 0x1.1a35beb6fcb75p+0, 0x1.1d4873168b9aap+0, 0x1.2063b88628cd6p+0,
+    0x1.2387a6e756238p+0, 0x1.26b4565e27cddp+0, 0x1.29e9df51fdee1p+0, 0x1.2d285a6e4030bp+0,
+    0x1.306fe0a31b715p+0, 0x1.33c08b26416ffp+0, 0x1.371a7373aa9cbp+0, 0x1.3a7db34e59ff7p+0,
+    0x1.3dea64c123422p+0, 0x1.4160a21f72e2ap+0, 0x1.44e086061892dp+0, 0x1.486a2b5c13cd0p+0,
+    0x1.4bfdad5362a27p+0, 0x1.4f9b2769d2ca7p+0, 0x1.5342b569d4f82p+0, 0x1.56f4736b527dap+0,
+    0x1.5ab07dd485429p+0, 0x1.5e76f15ad2148p+0, 0x1.6247eb03a5585p+0, 0x1.6623882552225p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.6dfb23c651a2fp+0, 0x1.71f75e8ec5f74p+0, 0x1.75feb564267c9p+0,
+    0x1.7a11473eb0187p+0, 0x1.7e2f336cf4e62p+0, 0x1.82589994cce13p+0, 0x1.868d99b4492edp+0,
+    0x1.8ace5422aa0dbp+0, 0x1.8f1ae99157736p+0, 0x1.93737b0cdc5e5p+0, 0x1.97d829fde4e50p+0,
+    0x1.9c49182a3f090p+0, 0x1.a0c667b5de565p+0, 0x1.a5503b23e255dp+0, 0x1.a9e6b5579fdbfp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b33a2b84f15fbp+0, 0x1.b7f76f2fb5e47p+0, 0x1.bcc1e904bc1d2p+0,
+    0x1.c199bdd85529cp+0, 0x1.c67f12e57d14bp+0, 0x1.cb720dcef9069p+0, 0x1.d072d4a07897cp+0,
+    0x1.d5818dcfba487p+0, 0x1.da9e603db3285p+0, 0x1.dfc97337b9b5fp+0, 0x1.e502ee78b3ff6p+0,
+    0x1.ea4afa2a490dap+0, 0x1.efa1bee615a27p+0, 0x1.f50765b6e4540p+0, 0x1.fa7c1819e90d8p+0};
 __device__ __forceinline__ void fill_roots(double *root) {
-    if (threadIdx.x < 64) root[threadIdx.x] = exp2((double)threadIdx.x / 64.0);
+    if (threadIdx.x < 64) root[threadIdx.x] = kRoots[threadIdx.x];
 }
 
 // What falls as x rises, 0 at the largest; both zeros are one.
@@ -122,26 +146,38 @@ template <typename T> __device__ __forceinline__ u64 place_of(float x, int i) {
     if constexpr (sizeof(T) == 2) return (u64)(key_of(x) >> 16) << 48 | (uint32_t)i;
     else return (u64)key_of(x) << 32 | (uint32_t)i;
 }
+// A place's key, in its own 32 or 16 bits, and its logit.
+template <typename T> __device__ __forceinline__ uint32_t place_key(u64 p) { return (uint32_t)(p >> (sizeof(T) == 2 ? 48 : 32)); }
+template <typename T> __device__ __forceinline__ uint32_t cut_key(uint32_t key) { return sizeof(T) == 2 ? key >> 16 : key; }
+template <typename T> __device__ __forceinline__ float place_value(u64 p) {
+    const uint32_t k = place_key<T>(p);
+    return of_key(sizeof(T) == 4 ? k : k >> 15 ? k << 16 : k << 16 | 0xffffu);
+}
 // The last place whose logit is `k` or larger.
 template <typename T> __device__ __forceinline__ u64 last_of_key(uint32_t k) {
     if constexpr (sizeof(T) == 2) return (u64)(k >> 31 ? k >> 16 : ((k + 1) >> 16) - 1) << 48 | 0xffffffffffffull;
     else return (u64)k << 32 | 0xffffffffull;
 }
 
-__device__ __forceinline__ u64 wave_sum(u64 x) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
-    return x;
+// Sums over the wave's lanes up to each, and over all, without a trip through
+// LDS.
+template <int CTRL, int ROWS> __device__ __forceinline__ u64 dpp_plus(u64 x) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), CTRL, ROWS, 0xf, false);
+    return x + ((u64)hi << 32 | lo);
 }
 __device__ __forceinline__ u64 wave_running(u64 x) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const u64 y = __shfl_up(x, m, 64);
-        if (lane >= m) x += y;
-    }
-    return x;
+    x = dpp_plus<0x111, 0xf>(x);   // from 1, 2, 4 and 8 lanes below within a row of 16
+    x = dpp_plus<0x112, 0xf>(x);
+    x = dpp_plus<0x114, 0xf>(x);
+    x = dpp_plus<0x118, 0xf>(x);
+    x = dpp_plus<0x142, 0xa>(x);   // a row's last lane to the next row
+    return dpp_plus<0x143, 0xc>(x);   // lane 31 to the upper half
 }
+__device__ __forceinline__ u64 of_lane(u64 x, int lane) {
+    return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+}
+__device__ __forceinline__ u64 wave_sum(u64 x) { return of_lane(wave_running(x), 63); }
 
 // The largest of a workgroup's values and the first index that has it, in
 // every thread.
@@ -170,7 +206,7 @@ template <int WAVES> __device__ __forceinline__ void block_top(float &top, int &
 
 // ---- first launch: the parts -------------------------------------------------
 
-struct Part { float top; int at, bin, pad; };
+struct Part { float top; int at, bin, count; u64 mass; };   // count and mass of all its bins
 enum Kind : int { kNothing, kLargest, kDrawn };
 struct Chosen { u64 cut, total; float top; int at, kind, pad; };
 
@@ -200,42 +236,70 @@ __device__ __forceinline__ Limits limits_of(const SampleArgs &a, long n) {
     return y;
 }
 
+// kCopies histograms side by side, a lane's by its number, keep lanes that meet in
+// a bin apart.
+constexpr int kCopies = 4;
 template <typename T> __global__ __launch_bounds__(kPartThreads) void parts_kernel(const SampleArgs a, const Work w, int bits) {
-    __shared__ uint32_t count[kBins];
-    __shared__ u64 mass[kBins];
+    __shared__ uint32_t count[kBins * kCopies];
+    __shared__ u64 mass[kBins * kCopies];
     __shared__ double root[64];
     __shared__ float tops[kPartThreads / 64];
     __shared__ int ats[kPartThreads / 64];
+    static_assert(kPartThreads == kBins, "a bin a thread");
     const int tid = threadIdx.x, lo = (blockIdx.x % w.parts) * w.length, hi = min(lo + w.length, a.vocab);
     const long n = blockIdx.x / w.parts;
     const T *x = static_cast<const T *>(a.logits) + n * a.stride;
     const Limits lim = limits_of(a, n);
-    count[tid] = 0;
-    mass[tid] = 0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        count[tid + i * kBins] = 0;
+        mass[tid + i * kBins] = 0;
+    }
     fill_roots(root);
     float top = -__builtin_inff();
     int at = INT32_MAX;
-    each_of<kPartThreads>(x, lo, hi, [&](float y, int i) {
+    each_of<kPartThreads, 4>(x, lo, hi, [&](float y, int i) {
         if (y > top || (y == top && i < at)) {
             top = y;
             at = i;
         }
     });
     block_top(top, at, tops, ats);
-    const bool some = top > -__builtin_inff() && lim.temperature > 0.f;
+    if (!(top > -__builtin_inff()) || !(lim.temperature > 0.f)) {
+        if (tid == 0) w.part[blockIdx.x] = Part{top, at, 0, 0, 0};
+        return;
+    }
     const Row row = row_at(top, lim.temperature, bits, root);
-    const int first = some ? row.bin(top) : 0;
-    if (tid == 0) w.part[blockIdx.x] = Part{top, at, first, 0};
-    if (!some) return;
-    each_of<kPartThreads>(x, lo, hi, [&](float y, int) {
-        if (y != y) return;
-        const int b = (int)min((uint32_t)(first - row.bin(y)), (uint32_t)kBins - 1);
-        atomicAdd(&count[b], 1u);
-        if (!lim.counts) atomicAdd(&mass[b], row.weight(y));
-    });
+    const int first = row.bin(top), copy = tid & (kCopies - 1);
+    const auto count_all = [&](auto counts, auto weighs) {
+        each_of<kPartThreads, 2>(x, lo, hi, [&](float y, int) {
+            if (y != y) return;
+            const int b = (int)min((uint32_t)(first - row.bin(y)), (uint32_t)kBins - 1) * kCopies + copy;
+            if constexpr (decltype(counts)::value) atomicAdd(&count[b], 1u);
+            if constexpr (decltype(weighs)::value) atomicAdd(&mass[b], row.weight(y));
+        });
+    };
+    if (lim.counts) count_all(std::true_type{}, std::false_type{});
+    else if (lim.by_k) count_all(std::true_type{}, std::true_type{});
+    else count_all(std::false_type{}, std::true_type{});
     __syncthreads();
-    w.count[(long)blockIdx.x * kBins + tid] = count[tid];
-    if (!lim.counts) w.mass[(long)blockIdx.x * kBins + tid] = mass[tid];
+    u64 c = 0, m = 0;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        c += count[tid * kCopies + i];
+        m += mass[tid * kCopies + i];
+    }
+    if (lim.by_k) w.count[(long)blockIdx.x * kBins + tid] = (uint32_t)c;
+    if (!lim.counts) w.mass[(long)blockIdx.x * kBins + tid] = m;
+    __syncthreads();
+    c = wave_sum(c);
+    m = wave_sum(m);
+    if ((tid & 63) == 0) {
+        count[tid >> 6] = (uint32_t)c;
+        mass[tid >> 6] = m;
+    }
+    __syncthreads();
+    if (tid == 0) w.part[blockIdx.x] = Part{top, at, first, (int)(count[0] + count[1] + count[2] + count[3]), mass[0] + mass[1] + mass[2] + mass[3]};
 }
 
 // ---- second launch: the cut and the token --------------------------------------
@@ -243,8 +307,8 @@ template <typename T> __global__ __launch_bounds__(kPartThreads) void parts_kern
 struct Shared {
     uint32_t count[kFine];
     u64 mass[kFine];
-    u64 list[kList];
-    u64 sorted[kFew], sorted_mass[kFew];
+    u64 list[kList], list_mass[kList];
+    u64 few[kFew], few_mass[kFew], sorted[kFew], sorted_mass[kFew];
     uint32_t rank[kFew];
     double root[64];
     uint32_t digit[256];
@@ -253,9 +317,7 @@ struct Shared {
     double factor[kMostParts];
     int shift[kMostParts];
     u64 out[4];
-    float tops[kWaves];
-    int ats[kWaves];
-    int listed;
+    int listed, found;
 };
 
 // The first of n numbers (n a multiple of 64) with which their running sum is
@@ -269,10 +331,10 @@ template <typename N> __device__ __forceinline__ int first_reaching(const N *at,
         const u64 reach = __ballot(incl >= want);
         if (reach) {
             const int k = __builtin_ctzll(reach);
-            before = __shfl(incl - own, k, 64);
+            before = of_lane(incl - own, k);
             return i + k;
         }
-        sum = __shfl(incl, 63, 64);
+        sum = of_lane(incl, 63);
     }
     before = sum;
     return n;
@@ -304,100 +366,222 @@ __device__ __forceinline__ u64 block_sum(Shared &sh, u64 x) {
     return x;
 }
 
-// Among the places each() goes over, the first at which the running count (or
-// sum of weights, BY_MASS) is at least `want`, digit by digit; `upto`: the sum of
-// weights up to it and its own.
-template <typename T, bool BY_MASS, typename Each>
-__device__ u64 select(Shared &sh, const Row &row, const Each &each, int index_bits, u64 want, u64 &upto) {
-    const int tid = threadIdx.x;
-    u64 prefix = 0, mask = 0;
-    upto = 0;
-    int shift = 56;
-    for (;;) {
-        if (tid < 256) {
-            sh.digit[tid] = 0;
-            sh.digit_mass[tid] = 0;
-        }
-        __syncthreads();
-        each([&](u64 place, float x) {
-            if ((place & mask) == prefix) {
-                const int d = (int)(place >> shift) & 255;
-                atomicAdd(&sh.digit[d], 1u);
-                atomicAdd(&sh.digit_mass[d], row.weight(x));
-            }
-        });
-        __syncthreads();
-        if (tid < 64) {
-            u64 before;
-            int d;
-            if constexpr (BY_MASS) d = min(first_reaching(sh.digit_mass, 256, want, before), 255);
-            else d = min(first_reaching(sh.digit, 256, want, before), 255);
-            u64 less = 0;   // weights of the digits below
-            for (int i = tid; i < d; i += 64) less += sh.digit_mass[i];
-            less = wave_sum(less);
-            if (tid == 0) {
-                sh.out[0] = d;
-                sh.out[1] = want - min(before, want);
-                sh.out[2] = less;
-                sh.out[3] = sh.digit_mass[d];
-            }
-        }
-        __syncthreads();
-        const u64 d = sh.out[0], own = sh.out[3];
-        want = sh.out[1];
-        upto += sh.out[2];
-        prefix |= d << shift;
-        mask |= (u64)255 << shift;
-        __syncthreads();
-        if (shift == 0) {
-            upto += own;
-            return prefix;
-        }
-        shift -= 8;
-        if (sizeof(T) == 2 && shift == 40) shift = 24;
-        if (shift < 32 && shift >= index_bits) shift = (index_bits - 1) / 8 * 8;
-    }
+// The least weights' sum that keeps top_p of all.
+__device__ __forceinline__ u64 share_of(float top_p, u64 all) {
+    return max(min((u64)__builtin_ceil((double)__builtin_fmaxf(top_p, 0.f) * (double)all), all), (u64)1);
 }
 
-// Up to kFew places of sh.list put in order, with their weights.
-template <typename T> __device__ __forceinline__ void sort_few(Shared &sh, const Row &row, const T *x, int n) {
-    const int tid = threadIdx.x;
+// n <= kFew places with their weights put in order, into sh.sorted: each
+// against the others, a quarter of them a thread.  BY_INDEX: in the order of
+// indices.
+template <bool BY_INDEX> __device__ __forceinline__ void sort_few(Shared &sh, const u64 *from, const u64 *weights, int n) {
+    const int tid = threadIdx.x, mine = tid & (kFew - 1), lo = tid / kFew * (kFew / 4), hi = min(lo + kFew / 4, n);
+    const auto order = [](u64 p) { return BY_INDEX ? (uint32_t)p : p; };
     if (tid < kFew) sh.rank[tid] = 0;
     __syncthreads();
-    // every place against the others, a quarter of them a thread
-    const int mine = tid & (kFew - 1), from = tid / kFew * (kFew / 4), to = min(from + kFew / 4, n);
-    const u64 p = sh.list[mine];
     if (mine < n) {
+        const u64 p = order(from[mine]);
         uint32_t r = 0;
-        for (int i = from; i < to; ++i) r += sh.list[i] < p;
+#pragma unroll 8
+        for (int i = lo; i < hi; ++i) r += order(from[i]) < p;
         if (r) atomicAdd(&sh.rank[mine], r);
     }
     __syncthreads();
     if (tid < n) {
-        sh.sorted[sh.rank[tid]] = p;
-        sh.sorted_mass[sh.rank[tid]] = row.weight(value(x, (uint32_t)p));
+        sh.sorted[sh.rank[tid]] = from[tid];
+        sh.sorted_mass[sh.rank[tid]] = weights[tid];
     }
     __syncthreads();
 }
 
-// Gathers the places of a row's logits that in() picks into sh.list; as many as
-// the caller has counted.
-template <typename T, typename In> __device__ __forceinline__ void gather(Shared &sh, const T *x, int V, const In &in) {
-    if (threadIdx.x == 0) sh.listed = 0;
-    __syncthreads();
-    each_of<kThreads>(x, 0, V, [&](float y, int i) {
-        if (y == y && in(y)) {
+// How many of sh.sorted's first n stand before the running count (or sum of
+// weights, BY_MASS) is at least `want`, and the one with which it is; `upto`: the
+// sum of their weights.  By one wave, four a lane.
+template <bool BY_MASS> __device__ __forceinline__ int few_reaching(const Shared &sh, int n, u64 want, u64 &upto) {
+    const int lane = threadIdx.x & 63;
+    u64 y[4], s = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[i] = 4 * lane + i < n ? sh.sorted_mass[4 * lane + i] : 0;
+        s += y[i];
+    }
+    u64 run = wave_running(s) - s;
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = 4 * lane + i;
+        mine += k < n && (BY_MASS ? run < want : (u64)k < want);
+        run += y[i];
+    }
+    const int all = (int)wave_sum((u64)mine);
+    u64 kept = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (4 * lane + i < all) kept += y[i];
+    upto = wave_sum(kept);
+    return all;
+}
+
+// Among the places each() goes over, with keys in [lo, hi], the first at which the
+// running count (or sum of weights, BY_MASS) is at least `want`; `upto`: the sum of
+// weights up to it and its own.  A histogram of 256 equal pieces of the keys says in
+// which piece it lies, and so on until few are left, which are put in order; equal
+// keys are told apart by index.  BY_INDEX: the index is the key.  each(f) calls
+// f(place, a function that gives its weight).  ~0 where there is no place.
+template <typename T, bool BY_MASS, bool BY_INDEX, typename Each>
+__device__ u64 nth(Shared &sh, const Each &each, uint32_t lo, uint32_t hi, int V, u64 want, u64 &upto) {
+    const int tid = threadIdx.x;
+    bool tie = BY_INDEX;             // the index is looked at
+    uint32_t equal = 0;              // the key of those that are
+    u64 less = 0;                    // weights of what lies before [lo, hi]
+    for (;;) {
+        const uint32_t width = hi - lo;
+        const int s = max(0, 24 - __builtin_clz(width | 1));
+        const auto piece = [&](u64 p) -> int {     // of the range, or -1
+            if (!BY_INDEX && tie && place_key<T>(p) != equal) return -1;
+            const uint32_t k = (tie ? (uint32_t)p : place_key<T>(p)) - lo;
+            return k <= width ? (int)(k >> s) : -1;
+        };
+        if (tid < 256) {
+            sh.digit[tid] = 0;
+            sh.digit_mass[tid] = 0;
+        }
+        if (tid == 0) sh.found = 0;
+        __syncthreads();
+        each([&](u64 p, auto weight) {
+            const int d = piece(p);
+            if (d >= 0) {
+                atomicAdd(&sh.digit[d], 1u);
+                atomicAdd(&sh.digit_mass[d], weight());
+            }
+        });
+        __syncthreads();
+        if (tid < 64) {
+            u64 before, sum = 0;
+            int d;
+            if constexpr (BY_MASS) d = first_reaching(sh.digit_mass, 256, want, before);
+            else d = first_reaching(sh.digit, 256, want, before);
+            if (d == 256) {          // sums that differ in the last place: the last piece that has some
+                for (int i = 192; i >= 0 && d == 256; i -= 64) {
+                    const u64 some = __ballot(sh.digit[i + tid] > 0);
+                    if (some) d = i + 63 - __builtin_clzll(some);
+                }
+                d = d == 256 ? 0 : d;
+                before = BY_MASS ? before - sh.digit_mass[d] : before - sh.digit[d];
+            }
+            for (int i = tid; i < d; i += 64) sum += sh.digit_mass[i];
+            sum = wave_sum(sum);
+            if (tid == 0) {
+                sh.out[0] = d;
+                sh.out[1] = want - min(before, want);
+                sh.out[2] = sum;
+            }
+        }
+        __syncthreads();
+        const int d = (int)sh.out[0], some = (int)sh.digit[d];
+        want = sh.out[1];
+        less += sh.out[2];
+        if (some == 0) {
+            upto = less;
+            return ~0ull;
+        }
+        if (some <= kFew) {
+            each([&](u64 p, auto weight) {
+                if (piece(p) == d) {
+                    const int at = atomicAdd(&sh.found, 1);
+                    sh.few[at] = p;
+                    sh.few_mass[at] = weight();
+                }
+            });
+            __syncthreads();
+            sort_few<BY_INDEX>(sh, sh.few, sh.few_mass, some);
+            if (tid < 64) {
+                u64 sum;
+                const int k = few_reaching<BY_MASS>(sh, some, want, sum);
+                if (tid == 0) {
+                    sh.out[0] = sh.sorted[max(k, 1) - 1];
+                    sh.out[1] = sum;
+                }
+            }
+            __syncthreads();
+            const u64 p = sh.out[0];
+            upto = less + sh.out[1];
+            __syncthreads();
+            return p;
+        }
+        __syncthreads();
+        lo += (uint32_t)d << s;
+        hi = min(hi, lo + ((1u << s) - 1));
+        if (s == 0) {                // one key, and more than a few that have it
+            equal = lo;
+            tie = true;
+            lo = 0;
+            hi = (uint32_t)V - 1;
+        }
+    }
+}
+
+// The last key of [lo, hi) for which holds() is true; it is true at lo and, once
+// false, stays false.  By one wave.
+template <typename Holds> __device__ __forceinline__ uint32_t last_key(uint32_t lo, uint32_t hi, const Holds &holds) {
+    const int lane = threadIdx.x & 63;
+    while (hi - lo > 1) {
+        const uint32_t step = (hi - lo + 63) / 64;
+        const u64 k = (u64)lo + (u64)step * lane;
+        const int last = 63 - __builtin_clzll(__ballot(k < hi && (lane == 0 || holds((uint32_t)k))));
+        hi = (uint32_t)min((u64)lo + (u64)step * (last + 1), (u64)hi);
+        lo += step * last;
+    }
+    return lo;
+}
+constexpr uint32_t kMinusInfinity = 0xff800000u;   // its key: the last of all
+
+// The row's logits in [from, to] into sh.list, with their weights; as many as the
+// caller has counted.
+template <typename T> __device__ __forceinline__ void gather(Shared &sh, const Row &row, const T *x, int V, float from, float to) {
+    constexpr int N = 16 / (int)sizeof(T), AHEAD = 4;
+    const int tid = threadIdx.x, head = min(V, (int)((0 - reinterpret_cast<uintptr_t>(x)) % 16 / sizeof(T))), wide = (V - head) / N;
+    const auto take = [&](int i) {
+        const float y = value(x, i);
+        if (y >= from && y <= to) {
             const int at = atomicAdd(&sh.listed, 1);
             if (at < kList) sh.list[at] = place_of<T>(y, i);
         }
-    });
+    };
+    if (tid == 0) sh.listed = 0;
+    __syncthreads();
+    if (tid < head) take(tid);
+    for (int v = tid; v < wide; v += AHEAD * kThreads) {
+        u32x4 w[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) w[k] = *reinterpret_cast<const u32x4 *>(x + head + (long)min(v + k * kThreads, wide - 1) * N);
+        uint32_t in = 0;             // few are taken: one look at 32 of them
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float y;
+                if constexpr (N == 4) y = __uint_as_float(w[k][e]);
+                else y = __uint_as_float(e & 1 ? w[k][e / 2] & 0xffff0000u : w[k][e / 2] << 16);
+                in |= (uint32_t)(y >= from && y <= to) << (k * N + e);
+            }
+        while (in) {
+            const int e = __builtin_ctz(in);
+            in &= in - 1;
+            if (v + e / N * kThreads < wide) take(head + (v + e / N * kThreads) * N + e % N);
+        }
+    }
+    const int tail = head + wide * N;
+    if (tail + tid < V) take(tail + tid);
+    __syncthreads();
+    for (int i = tid; i < min(sh.listed, kList); i += kThreads) sh.list_mass[i] = row.weight(place_value<T>(sh.list[i]));
     __syncthreads();
 }
 
 // The cut of a row whatever its logits, from passes over all of it: for rows
 // with more logits in the cut's bin than the list holds (thousands of equal
 // ones, or a cut far down).
-template <typename T> __device__ u64 cut_of_whole_row(Shared &sh, const Row &row, const Limits &lim, const T *x, int V, int index_bits) {
+template <typename T> __device__ u64 cut_of_whole_row(Shared &sh, const Row &row, const Limits &lim, const T *x, int V) {
     const int tid = threadIdx.x;
     // bins of (top - x) / T, 64 a unit
     const float rate = 64.f / lim.temperature;
@@ -422,10 +606,10 @@ template <typename T> __device__ u64 cut_of_whole_row(Shared &sh, const Row &row
         const auto each = [&](auto f) {
             for (int i = tid; i < V; i += kThreads) {
                 const float y = value(x, i);
-                if (y == y && bin(y) == b) f(place_of<T>(y, i), y);
+                if (y == y && bin(y) == b) f(place_of<T>(y, i), [&] { return row.weight(y); });
             }
         };
-        return select<T, decltype(by_mass)::value>(sh, row, each, index_bits, want, upto);
+        return nth<T, decltype(by_mass)::value, false>(sh, each, cut_key<T>(key_of(row.top)), cut_key<T>(kMinusInfinity), V, want, upto);
     };
     u64 cut = ~0ull, before, upto = 0;
     int last = kFine;
@@ -436,11 +620,9 @@ template <typename T> __device__ u64 cut_of_whole_row(Shared &sh, const Row &row
     if (lim.by_p) {
         u64 s = 0;
         for (int i = tid; i < last; i += kThreads) s += sh.mass[i];
-        const u64 total = block_sum(sh, s) + upto;
-        const double part = (double)__builtin_fmaxf(lim.top_p, 0.f) * (double)total;
-        const u64 want = max(min((u64)__builtin_ceil(part), total), (u64)1);
+        const u64 want = share_of(lim.top_p, block_sum(sh, s) + upto);
         const int b = block_reaching(sh, sh.mass, kFine, want, before);
-        cut = min(cut, cut_in(min(b, kFine - 1), std::true_type{}, want - before, upto));
+        cut = min(cut, cut_in(min(b, kFine - 1), std::true_type{}, want - min(before, want), upto));
     }
     return cut;
 }
@@ -451,15 +633,31 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
     const long n = blockIdx.x;
     const T *x = static_cast<const T *>(a.logits) + n * a.stride;
     const Limits lim = limits_of(a, n);
-    const Part *parts = w.part + n * w.parts;
-
-    float top = -__builtin_inff();
-    int at = INT32_MAX;
-    for (int p = 0; p < w.parts; ++p)
-        if (parts[p].top > top) {
-            top = parts[p].top;
-            at = parts[p].at;
+    // the parts' bins, one a thread of a quarter of the parts each: asked for before
+    // anything else, as they come from far
+    constexpr int QUARTER = kThreads / kBins, EACH = kMostParts / QUARTER;
+    const int own_bin = tid & (kBins - 1), own_part = tid / kBins;
+    uint32_t part_count[EACH];
+    u64 part_mass[EACH];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const long from = (n * w.parts + min(own_part + k * QUARTER, w.parts - 1)) * kBins + own_bin;
+        part_count[k] = lim.by_k ? w.count[from] : 0;
+        part_mass[k] = lim.counts ? 0 : w.mass[from];
+    }
+    // a part a lane
+    const Part mine = lane < w.parts ? w.part[n * w.parts + lane] : Part{-__builtin_inff(), INT32_MAX, 0, 0, 0};
+    float top = mine.top;
+    int at = mine.at;
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) {
+        const float y = __shfl_xor(top, m, 64);
+        const int j = __shfl_xor(at, m, 64);
+        if (y > top || (y == top && j < at)) {
+            top = y;
+            at = j;
         }
+    }
     if (!(top > -__builtin_inff()) || !(lim.temperature > 0.f)) {   // no logit at all, or the largest
         if (tid == 0) {
             const bool none = !(top > -__builtin_inff());
@@ -470,29 +668,45 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
     }
     fill_roots(sh.root);
     const Row row = row_at(top, lim.temperature, bits, sh.root);
-    const int first = row.bin(top), index_bits = 32 - __builtin_clz(max(V - 1, 1));
+    const int first = row.bin(top);
     const auto bin = [&](float y) { return (int)min((uint32_t)(first - row.bin(y)), (uint32_t)kBins - 1); };
-    __syncthreads();
-    // the parts' bins and weights against the row's largest
-    if (tid < w.parts) {
-        sh.shift[tid] = min(first - parts[tid].bin, kBins - 1);
-        sh.factor[tid] = parts[tid].top > -__builtin_inff() ? row.real(parts[tid].top) / row.one : -1.0;   // -1: nothing there
-    }
     if (tid < kBins) {
         sh.count[tid] = 0;
         sh.mass[tid] = 0;
     }
     __syncthreads();
+    // the parts' bins and weights against the row's largest
+    if (tid < kMostParts) {
+        sh.shift[tid] = min(first - mine.bin, kBins - 1);
+        sh.factor[tid] = mine.top > -__builtin_inff() ? row.real(mine.top) / row.one : -1.0;   // -1: nothing there
+    }
+    __syncthreads();
     if (lim.by_k || lim.by_p) {
-        const int j = tid & (kBins - 1);
-        for (int p = tid / kBins; p < w.parts; p += kThreads / kBins) {
-            if (sh.factor[p] < 0.0) continue;
-            const long from = (n * w.parts + p) * kBins + j;
-            const uint32_t y = w.count[from];
-            const u64 z = lim.counts ? 0 : (u64)__builtin_rint((double)w.mass[from] * sh.factor[p]);
-            const int to = min(j + sh.shift[p], kBins - 1);
-            atomicAdd(&sh.count[to], y);
-            if (!lim.counts) atomicAdd(&sh.mass[to], z);
+        // the last bin has what is left of the sums
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            const int p = own_part + k * QUARTER;
+            if (p >= w.parts || sh.factor[p] < 0.0) continue;
+            const int to = own_bin + sh.shift[p];
+            if (to >= kBins - 1) continue;
+            if (part_count[k]) atomicAdd(&sh.count[to], part_count[k]);
+            if (part_mass[k]) atomicAdd(&sh.mass[to], (u64)__builtin_rint((double)part_mass[k] * sh.factor[p]));
+        }
+        __syncthreads();
+        if (wave == 0) {
+            u64 cs = 0, ms = 0;
+            for (int i = lane; i < kBins - 1; i += 64) {
+                cs += sh.count[i];
+                ms += sh.mass[i];
+            }
+            cs = wave_sum(cs);
+            ms = wave_sum(ms);
+            const u64 call = wave_sum(sh.factor[lane] < 0.0 ? 0 : (u64)mine.count);
+            const u64 mall = wave_sum(lim.counts || sh.factor[lane] < 0.0 ? 0 : (u64)__builtin_rint((double)mine.mass * sh.factor[lane]));
+            if (lane == 0) {
+                sh.count[kBins - 1] = (uint32_t)(call - cs);
+                sh.mass[kBins - 1] = mall > ms ? mall - ms : 0;
+            }
         }
         __syncthreads();
     }
@@ -501,21 +715,23 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
     if (lim.by_m) {                  // the smallest number whose weight is not below the limit
         if (wave == 0) {
             const double least = (double)lim.min_p * row.one;
-            uint32_t lo = key_of(top), hi = 0xff800000u;   // holds; does not (minus infinity weighs nothing)
-            while (hi - lo > 1) {
-                const uint32_t step = (hi - lo + 63) / 64;
-                const uint32_t k = (uint32_t)min((u64)lo + (u64)step * lane, (u64)hi);
-                const u64 holds = __ballot(k < hi && (k == lo || row.real(of_key(k)) >= least));
-                const int last = 63 - __builtin_clzll(holds);
-                hi = (uint32_t)min((u64)lo + (u64)step * (last + 1), (u64)hi);
-                lo += step * last;
-            }
-            if (lane == 0) sh.out[0] = last_of_key<T>(lo);
+            const uint32_t k = last_key(key_of(top), kMinusInfinity, [&](uint32_t k) { return row.real(of_key(k)) >= least; });
+            if (lane == 0) sh.out[0] = last_of_key<T>(k);
         }
         __syncthreads();
         cut = sh.out[0];
         __syncthreads();
     }
+    // the smallest logit of bins up to b (b >= 0)
+    const auto end_of = [&](int b) {
+        if (b >= kBins - 1) return kMinusInfinity;
+        return last_key(key_of(top), kMinusInfinity + 1, [&](uint32_t k) { return bin(of_key(k)) <= b; });
+    };
+    const auto listed_each = [&](auto f) {
+        const int some = sh.listed;
+        for (int i = tid; i < some; i += kThreads) f(sh.list[i], [&] { return sh.list_mass[i]; });
+    };
+    const uint32_t key_lo = cut_key<T>(key_of(top));
 
     bool whole = false;              // the list cannot hold a cut's bin
     u64 total = 0;                   // of the weights kept
@@ -523,47 +739,27 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
         // few are kept: all logits up to the bin of the k-th
         u64 before;
         const int b = min(block_reaching(sh, sh.count, kBins, (u64)lim.top_k, before), kBins - 1);
-        u64 c = tid <= b ? sh.count[tid] : 0;
-        const int some = (int)min(block_sum(sh, c), (u64)kList + 1);
-        whole = some > kList;
+        whole = block_sum(sh, tid <= b ? sh.count[tid] : 0) > (u64)kList;
         if (!whole) {
-            gather(sh, x, V, [&](float y) { return bin(y) <= b; });
+            const uint32_t end = end_of(b);
+            gather(sh, row, x, V, of_key(end), top);
+            const int some = sh.listed;
             if (some <= kFew) {
-                sort_few(sh, row, x, some);
-                int keep = min(some, lim.top_k);
+                sort_few<false>(sh, sh.list, sh.list_mass, some);
                 if (wave == 0) {
-                    // running sums, four a lane
-                    u64 y[4], s = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[i] = 4 * lane + i < keep ? sh.sorted_mass[4 * lane + i] : 0;
-                        s += y[i];
-                    }
-                    const u64 incl = wave_running(s), all = __shfl(incl, 63, 64);
-                    u64 want = all;
-                    if (lim.by_p) want = max(min((u64)__builtin_ceil((double)__builtin_fmaxf(lim.top_p, 0.f) * (double)all), all), (u64)1);
-                    u64 run = incl - s;
-                    int mine = 0;      // of this lane's four, those kept
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = 4 * lane + i;
-                        if (k < keep && (!lim.by_p || run < want) && sh.sorted[k] <= cut) ++mine;
-                        run += y[i];
-                    }
-#pragma unroll
-                    for (int m = 32; m >= 1; m >>= 1) mine += __shfl_xor(mine, m, 64);
-                    u64 kept = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * lane + i < mine) kept += y[i];
-                    kept = wave_sum(kept);
+                    u64 all, upto;
+                    int keep = few_reaching<false>(sh, some, (u64)lim.top_k, all);
+                    if (lim.by_p) keep = few_reaching<true>(sh, keep, share_of(lim.top_p, all), upto);
+                    if (lim.by_m)
+                        while (sh.sorted[keep - 1] > cut) --keep;
+                    few_reaching<false>(sh, keep, (u64)keep, upto);
                     if (lane == 0) {
-                        sh.out[0] = mine;
-                        sh.out[1] = kept;
+                        sh.out[0] = keep;
+                        sh.out[1] = upto;
                     }
                 }
                 __syncthreads();
-                keep = (int)sh.out[0];
+                const int keep = (int)sh.out[0];
                 total = sh.out[1];
                 cut = sh.sorted[keep - 1];
                 if (a.tokens && tid < keep) {
@@ -572,200 +768,117 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
                     const uint32_t i = (uint32_t)sh.sorted[tid];
                     const u64 own = sh.sorted_mass[tid];
                     u64 below = 0;
+#pragma unroll 4
                     for (int j = 0; j < keep; ++j)
                         if ((uint32_t)sh.sorted[j] < i) below += sh.sorted_mass[j];
                     if (below <= want && below + own > want) a.tokens[n] = (int)i;
                 }
-                if (tid == 0) w.row[n] = Chosen{cut, total, top, at, kDrawn, 0};
-                return;
-            }
-            const auto each = [&](auto f) {
-                for (int i = tid; i < some; i += kThreads) {
-                    const u64 p = sh.list[i];
-                    f(p, value(x, (uint32_t)p));
-                }
-            };
-            u64 all;
-            if (some > lim.top_k) {
-                cut = min(cut, select<T, false>(sh, row, each, index_bits, (u64)lim.top_k, all));
             } else {
+                u64 all, upto;
+                if (some > lim.top_k) {
+                    cut = min(cut, nth<T, false, false>(sh, listed_each, key_lo, cut_key<T>(end), V, (u64)lim.top_k, all));
+                } else {
+                    u64 s = 0;
+                    listed_each([&](u64, auto weight) { s += weight(); });
+                    all = block_sum(sh, s);
+                }
+                if (lim.by_p) cut = min(cut, nth<T, true, false>(sh, listed_each, key_lo, cut_key<T>(end), V, share_of(lim.top_p, all), upto));
                 u64 s = 0;
-                each([&](u64, float y) { s += row.weight(y); });
-                all = block_sum(sh, s);
-            }
-            if (lim.by_p) {
-                const u64 want = max(min((u64)__builtin_ceil((double)__builtin_fmaxf(lim.top_p, 0.f) * (double)all), all), (u64)1);
-                u64 upto;
-                cut = min(cut, select<T, true>(sh, row, each, index_bits, want, upto));
-            }
-            // drawn by index: the place is the index alone
-            u64 s = 0;
-            each([&](u64 p, float y) { s += p <= cut ? row.weight(y) : 0; });
-            total = block_sum(sh, s);
-            if (a.tokens) {
-                const auto by_index = [&](auto f) {
-                    each([&](u64 p, float y) {
-                        if (p <= cut) f((u64)(uint32_t)p, y);
-                    });
-                };
-                const u64 want = min((u64)((double)a.uniform[n] * (double)total), total - 1) + 1;
-                u64 upto;
-                const u64 i = select<float, true>(sh, row, by_index, index_bits, want, upto);
-                if (tid == 0) a.tokens[n] = (int)i;
+                listed_each([&](u64 p, auto weight) { s += p <= cut ? weight() : 0; });
+                total = block_sum(sh, s);
+                if (a.tokens) {
+                    const auto kept_each = [&](auto f) {
+                        listed_each([&](u64 p, auto weight) {
+                            if (p <= cut) f(p, weight);
+                        });
+                    };
+                    const u64 want = min((u64)((double)a.uniform[n] * (double)total), total - 1) + 1;
+                    const u64 p = nth<T, true, true>(sh, kept_each, 0, (uint32_t)V - 1, V, want, upto);
+                    if (tid == 0) a.tokens[n] = (int)(uint32_t)p;
+                }
             }
             if (tid == 0) w.row[n] = Chosen{cut, total, top, at, kDrawn, 0};
             return;
         }
     }
     int edge = kBins;                // the bin that the cut goes through: those before it are kept whole
-    int listed = -1;                 // the bin whose logits the list holds, in order where they are few
+    int listed = -1;                 // the bin whose logits the list holds
+    uint32_t list_lo = 0, list_hi = 0;   // and their keys
     if (!lim.counts) {
-        const auto list = [&](int b) {
-            if (listed == b) return;
-            gather(sh, x, V, [&](float y) { return bin(y) == b; });
-            if (sh.listed <= kFew) sort_few(sh, row, x, sh.listed);
+        const auto list = [&](int b) {   // true where it holds them all
+            if (listed == b) return true;
+            if (wave < 2) {
+                const uint32_t k = wave == 0 ? end_of(b) : b > 0 ? end_of(b - 1) + 1 : key_of(top);
+                if (lane == 0) sh.out[wave] = k;
+            }
+            __syncthreads();
+            list_hi = (uint32_t)sh.out[0];
+            list_lo = (uint32_t)sh.out[1];
+            __syncthreads();
+            gather(sh, row, x, V, of_key(list_hi), of_key(list_lo));
             listed = b;
+            return sh.listed <= kList;
         };
-        const auto cut_in = [&](int b, auto by_mass, u64 want, u64 &upto) -> u64 {
-            constexpr bool MASS = decltype(by_mass)::value;
-            list(b);
-            const int some = sh.listed;
-            upto = 0;
-            if (some == 0) return ~0ull;   // sums that differ in the last place ended up behind the last logit
-            if (some > kFew) {
-                const auto each = [&](auto f) {
-                    for (int i = tid; i < some; i += kThreads) {
-                        const u64 p = sh.list[i];
-                        f(p, value(x, (uint32_t)p));
-                    }
-                };
-                return select<T, MASS>(sh, row, each, index_bits, want, upto);
-            }
-            if (wave == 0) {
-                u64 y[4], s = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[i] = 4 * lane + i < some ? sh.sorted_mass[4 * lane + i] : 0;
-                    s += y[i];
-                }
-                u64 run = wave_running(s) - s;
-                int mine = 0;      // of this lane's four, those kept
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = 4 * lane + i;
-                    if (k < some && (MASS ? run < want : (u64)k < want)) ++mine;
-                    run += y[i];
-                }
-#pragma unroll
-                for (int m = 32; m >= 1; m >>= 1) mine += __shfl_xor(mine, m, 64);
-                u64 kept = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * lane + i < mine) kept += y[i];
-                kept = wave_sum(kept);
-                if (lane == 0) {
-                    sh.out[0] = sh.sorted[max(mine - 1, 0)];
-                    sh.out[1] = kept;
-                }
-            }
-            __syncthreads();
-            const u64 c = sh.out[0];
-            upto = sh.out[1];
-            __syncthreads();
-            return c;
+        const auto cut_in = [&](auto by_mass, u64 want, u64 &upto) {
+            return nth<T, decltype(by_mass)::value, false>(sh, listed_each, cut_key<T>(list_lo), cut_key<T>(list_hi), V, want, upto);
         };
         u64 before, upto = 0;
         int last = kBins;
         if (lim.by_k) {
             last = block_reaching(sh, sh.count, kBins, (u64)lim.top_k, before);
             if (last < kBins) {
-                whole = sh.count[last] > (uint32_t)kList;
+                whole = !list(last);
                 if (!whole) {
-                    cut = min(cut, cut_in(last, std::false_type{}, (u64)lim.top_k - before, upto));
+                    cut = min(cut, cut_in(std::false_type{}, (u64)lim.top_k - before, upto));
                     edge = last;
                 }
             }
         }
         if (lim.by_p && !whole) {
-            const u64 all = block_sum(sh, tid < last && tid < kBins ? sh.mass[tid] : 0) + upto;
-            const u64 want = max(min((u64)__builtin_ceil((double)__builtin_fmaxf(lim.top_p, 0.f) * (double)all), all), (u64)1);
+            const u64 want = share_of(lim.top_p, block_sum(sh, tid < last && tid < kBins ? sh.mass[tid] : 0) + upto);
             const int b = min(block_reaching(sh, sh.mass, kBins, want, before), kBins - 1);
-            whole = sh.count[b] > (uint32_t)kList;
+            whole = !list(b);
             if (!whole) {
-                cut = min(cut, cut_in(b, std::true_type{}, want - min(before, want), upto));
+                cut = min(cut, cut_in(std::true_type{}, want - min(before, want), upto));
                 edge = min(edge, b);
             }
         }
-        if (lim.by_m && !whole) {    // the bin of the limit's own number; the list may not hold it
-            const uint32_t k = (uint32_t)(cut >> 32);
-            const float y = of_key(sizeof(T) == 2 ? (k >> 31 ? k & 0xffff0000u : k | 0xffffu) : k);
-            if (bin(y) < edge) {
-                edge = bin(y);
-                u64 c = 0;
-                if (!(lim.by_k || lim.by_p)) {   // its bins were not brought together
-                    const int p = tid;
-                    if (p < w.parts && sh.factor[p] >= 0.0) {
-                        const int j = edge - sh.shift[p];
-                        if (edge < kBins - 1) c = j >= 0 ? w.count[(n * w.parts + p) * kBins + j] : 0;
-                        else
-                            for (int i = max(j, 0); i < kBins; ++i) c += w.count[(n * w.parts + p) * kBins + i];
-                    }
-                    c = block_sum(sh, c);
-                } else {
-                    c = sh.count[edge];
-                }
-                whole = c > (u64)kList;
-            }
-        }
-        if (!whole && edge < kBins) list(edge);
+        if (lim.by_m && !whole) edge = min(edge, bin(place_value<T>(cut)));   // the limit's own number may lie before
+        if (!whole && edge < kBins) whole = !list(edge);
     }
     if (whole) {
         __syncthreads();
         const u64 least = cut;
-        cut = min(lim.by_m ? least : ~0ull, cut_of_whole_row(sh, row, lim, x, V, index_bits));
+        cut = min(lim.by_m ? least : ~0ull, cut_of_whole_row(sh, row, lim, x, V));
     }
 
-    const auto kept = [&](int i) -> u64 {
-        const float y = value(x, i);
-        return y == y && place_of<T>(y, i) <= cut ? row.weight(y) : 0;
-    };
+    const auto kept = [&](float y, int i) -> u64 { return y == y && place_of<T>(y, i) <= cut ? row.weight(y) : 0; };
     int lo = 0, hi = V;
     u64 want = 0;
     if (!whole) {
         // what every part keeps: its bins before the cut's, and its share of the list
-        if (listed >= 0) {
-            if (tid < kMostParts) sh.part_mass[tid] = 0;
-            __syncthreads();
-            const int some = sh.listed;
-            for (int i = tid; i < some; i += kThreads) {
-                const u64 p = sh.list[i];
-                if (p <= cut) {
-                    const float y = value(x, (uint32_t)p);
-                    if (bin(y) == edge) atomicAdd(&sh.part_mass[(uint32_t)p / (uint32_t)w.length], row.weight(y));
-                }
-            }
-            __syncthreads();
+        if (tid < kMostParts) sh.part_mass[tid] = 0;
+        __syncthreads();
+        if (listed >= 0)
+            listed_each([&](u64 p, auto weight) {
+                if (p <= cut) atomicAdd(&sh.part_mass[(uint32_t)p / (uint32_t)w.length], weight());
+            });
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            const int p = own_part + k * QUARTER;
+            if (p >= w.parts || sh.factor[p] < 0.0) continue;
+            const bool in = edge == kBins || min(own_bin + sh.shift[p], kBins - 1) < edge;
+            const u64 s = wave_sum(in ? (u64)__builtin_rint((double)part_mass[k] * sh.factor[p]) : 0);
+            if (lane == 0 && s) atomicAdd(&sh.part_mass[p], s);
         }
-        for (int p = wave; p < w.parts; p += kWaves) {
-            if (sh.factor[p] < 0.0) {
-                if (lane == 0) sh.part_mass[p] = 0;
-                continue;
-            }
-            u64 s = 0;
-            for (int j = lane; j < kBins; j += 64)
-                if (edge == kBins || min(j + sh.shift[p], kBins - 1) < edge) s += w.mass[(n * w.parts + p) * kBins + j];
-            s = wave_sum(s);
-            if (lane == 0) sh.part_mass[p] = (u64)__builtin_rint((double)s * sh.factor[p]) + (listed >= 0 ? sh.part_mass[p] : 0);
-        }
-        if (tid < kMostParts && tid >= w.parts) sh.part_mass[tid] = 0;
         __syncthreads();
         if (wave == 0) {
-            const u64 own = sh.part_mass[lane], incl = wave_running(own), all = __shfl(incl, 63, 64);
+            const u64 own = sh.part_mass[lane], incl = wave_running(own), all = of_lane(incl, 63);
             u64 to = 0;
             if (a.tokens) to = min((u64)((double)a.uniform[n] * (double)all), all - 1);
             const u64 past = __ballot(incl > to);
             const int p = past ? __builtin_ctzll(past) : 0;
-            const u64 rest = to - __shfl(incl - own, p, 64);
+            const u64 rest = to - of_lane(incl - own, p);
             if (lane == 0) {
                 sh.out[0] = p;
                 sh.out[1] = rest;
@@ -778,14 +891,22 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
         want = sh.out[1];
         total = sh.out[2];
         __syncthreads();
+        if (tid == 0) w.row[n] = Chosen{cut, total, top, at, kDrawn, 0};
+        if (!a.tokens) return;
     }
-    if (tid == 0 && !whole) w.row[n] = Chosen{cut, total, top, at, kDrawn, 0};
-    if (!whole && !a.tokens) return;
     // by sixteenths of what is left of the row
     for (bool firstly = whole; firstly || hi - lo > 64; firstly = false) {
         const int each = (hi - lo + kWaves - 1) / kWaves, from = min(lo + wave * each, hi), to = min(from + each, hi);
         u64 s = 0;
-        for (int i = from + lane; i < to; i += 64) s += kept(i);
+        constexpr int AHEAD = 8;
+        for (int i = from + lane; i < to; i += 64 * AHEAD) {
+            float y[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) y[k] = value(x, min(i + 64 * k, to - 1));
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i + 64 * k < to) s += kept(y[k], i + 64 * k);
+        }
         s = wave_sum(s);
         if (lane == 0) sh.sums[wave] = s;
         __syncthreads();
@@ -803,7 +924,7 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
         __syncthreads();
     }
     if (wave == 0) {
-        const u64 own = lo + lane < hi ? kept(lo + lane) : 0, incl = wave_running(own);
+        const u64 own = lo + lane < hi ? kept(value(x, lo + lane), lo + lane) : 0, incl = wave_running(own);
         // the sums of parts and of their logits may differ in the last place: then the last one that weighs
         const u64 past = __ballot(incl > want), some = __ballot(own > 0);
         if (lane == 0) a.tokens[n] = lo + (past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : 0);
@@ -835,10 +956,11 @@ template <typename T> __global__ __launch_bounds__(kPartThreads) void probs_kern
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Parts of a row: enough workgroups for the chip, of 2048 logits or more.
+// Parts of a row: enough workgroups for the chip, of 2048 logits or more; of
+// 8192 at most, as the token's part is gone through again by one workgroup.
 void lay_out(Work &w, int rows, int vocab, void *workspace, size_t &bytes) {
     const long most = std::min<long>(kMostParts, (vocab + 2047) / 2048);
-    w.parts = (int)std::max<long>(1, std::min<long>(most, (1024 + rows - 1) / rows));
+    w.parts = (int)std::max<long>(1, std::min<long>(most, std::max<long>((1024 + rows - 1) / rows, vocab / 8192)));
     w.length = ((vocab + w.parts - 1) / w.parts + 7) / 8 * 8;
     w.parts = (vocab + w.length - 1) / w.length;
     const size_t cells = (size_t)rows * w.parts;
