@@ -71,29 +71,31 @@ template <int THREADS, int AHEAD, typename T, typename F> __device__ __forceinli
 struct Row {
     float top;              // the largest logit
     float bins;             // bins of one unit of logits
-    double rate;            // 64 log2(e) / T
+    double rate, shift;     // 64 log2(e) / T; top times that
     double one;             // 2^B
-    const double *root;     // 2^(j / 64)
+    const double *root;     // 2^(B + j / 64)
 
     // Rises with x, whatever x and the rate.
     __device__ __forceinline__ int bin(float x) const {
         constexpr float far = 536870912.f;
         return (int)__builtin_floorf(__builtin_fminf(__builtin_fmaxf(x * bins, -far), far));
     }
-    // 2^B exp((x - top) / T): 2^(k / 64) from a table and e^r, |r| <= ln 2 / 128,
-    // to r^5 (the rest is below 4e-17).
+    // 2^B exp((x - top) / T) = 2^(B + z / 64): 2^(B + k / 64) for k = z rounded from a
+    // table and its exponent, and 2^(r / 64), |r| <= 1/2, as its series to r^5 (the
+    // rest is below 4e-17).  One fused operation forms z, so that top * rate, which
+    // is rounded, is a factor that all weights but the largest have in common, off
+    // by 2^-53 |top / T|.  What is below 2^-1000 counts as that.
     __device__ __forceinline__ double real(float x) const {
-        if (x == top) return one;
-        const double z = ((double)x - (double)top) * rate;
-        if (!(z > -64.0 * 64.0)) return 0.0;
-        const double k = __builtin_rint(z), r = (z - k) * 0.010830424696249145;   // ln 2 / 64
+        const double z = __builtin_fmax(__builtin_fma((double)x, rate, -shift), -64000.0);
+        const double k = __builtin_rint(z), r = z - k;
+        double y = __builtin_fma(r, 0x1.5d87fe78a6730p-40, 0x1.3b2ab6fba4e77p-31);
+        y = __builtin_fma(r, y, 0x1.c6b08d704a0bfp-23);
+        y = __builtin_fma(r, y, 0x1.ebfbdff82c58ep-15);
+        y = __builtin_fma(r, y, 0x1.62e42fefa39efp-7);
+        y = __builtin_fma(r, y, 1.0);
         const int n = (int)k;
-        double y = __builtin_fma(r, 1.0 / 120.0, 1.0 / 24.0);
-        y = __builtin_fma(r, y, 1.0 / 6.0);
-        y = __builtin_fma(r, y, 0.5);
-        y = __builtin_fma(r, y, 1.0);
-        y = __builtin_fma(r, y, 1.0);
-        return __builtin_amdgcn_ldexp(y * root[n & 63], n >> 6) * one;
+        const u64 bits = __builtin_bit_cast(u64, y * root[n & 63]) + ((u64)(uint32_t)(n >> 6) << 52);
+        return x == top ? one : __builtin_bit_cast(double, bits);
     }
     // The same as a whole number.
     __device__ __forceinline__ u64 weight(float x) const {
@@ -106,6 +108,7 @@ __device__ __forceinline__ Row row_at(float top, float temperature, int bits, co
     r.top = top;
     r.bins = __builtin_fmaxf(__builtin_fminf(8.f * kLog2e / temperature, 1e30f), 1e-37f);   // an infinity stays one
     r.rate = 64.0 * 1.4426950408889634074 / (double)temperature;
+    r.shift = (double)top * r.rate;
     r.one = (double)(1ull << bits);
     r.root = root;
     return r;
@@ -129,8 +132,8 @@ __constant__ const double kRoots[64] = {
     0x1.c199bdd85529cp+0, 0x1.c67f12e57d14bp+0, 0x1.cb720dcef9069p+0, 0x1.d072d4a07897cp+0,
     0x1.d5818dcfba487p+0, 0x1.da9e603db3285p+0, 0x1.dfc97337b9b5fp+0, 0x1.e502ee78b3ff6p+0,
     0x1.ea4afa2a490dap+0, 0x1.efa1bee615a27p+0, 0x1.f50765b6e4540p+0, 0x1.fa7c1819e90d8p+0};
-__device__ __forceinline__ void fill_roots(double *root) {
-    if (threadIdx.x < 64) root[threadIdx.x] = kRoots[threadIdx.x];
+__device__ __forceinline__ void fill_roots(double *root, int bits) {
+    if (threadIdx.x < 64) root[threadIdx.x] = kRoots[threadIdx.x] * (double)(1ull << bits);
 }
 
 // What falls as x rises, 0 at the largest; both zeros are one.
@@ -255,7 +258,7 @@ template <typename T> __global__ __launch_bounds__(kPartThreads) void parts_kern
         count[tid + i * kBins] = 0;
         mass[tid + i * kBins] = 0;
     }
-    fill_roots(root);
+    fill_roots(root, bits);
     float top = -__builtin_inff();
     int at = INT32_MAX;
     each_of<kPartThreads, 4>(x, lo, hi, [&](float y, int i) {
@@ -666,7 +669,7 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
         }
         return;
     }
-    fill_roots(sh.root);
+    fill_roots(sh.root, bits);
     const Row row = row_at(top, lim.temperature, bits, sh.root);
     const int first = row.bin(top);
     const auto bin = [&](float y) { return (int)min((uint32_t)(first - row.bin(y)), (uint32_t)kBins - 1); };
@@ -834,16 +837,17 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
                 }
             }
         }
+        const int limit = lim.by_m ? bin(place_value<T>(cut)) : kBins;   // the bin of min_p's own number
         if (lim.by_p && !whole) {
             const u64 want = share_of(lim.top_p, block_sum(sh, tid < last && tid < kBins ? sh.mass[tid] : 0) + upto);
             const int b = min(block_reaching(sh, sh.mass, kBins, want, before), kBins - 1);
-            whole = !list(b);
-            if (!whole) {
+            if (b <= limit) whole = !list(b);
+            if (b <= limit && !whole) {
                 cut = min(cut, cut_in(std::true_type{}, want - min(before, want), upto));
                 edge = min(edge, b);
             }
         }
-        if (lim.by_m && !whole) edge = min(edge, bin(place_value<T>(cut)));   // the limit's own number may lie before
+        edge = min(edge, limit);
         if (!whole && edge < kBins) whole = !list(edge);
     }
     if (whole) {
@@ -867,9 +871,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
         for (int k = 0; k < EACH; ++k) {
             const int p = own_part + k * QUARTER;
             if (p >= w.parts || sh.factor[p] < 0.0) continue;
-            const bool in = edge == kBins || min(own_bin + sh.shift[p], kBins - 1) < edge;
-            const u64 s = wave_sum(in ? (u64)__builtin_rint((double)part_mass[k] * sh.factor[p]) : 0);
-            if (lane == 0 && s) atomicAdd(&sh.part_mass[p], s);
+            const u64 s = wave_sum(edge == kBins || min(own_bin + sh.shift[p], kBins - 1) < edge ? part_mass[k] : 0);
+            if (lane == 0 && s) atomicAdd(&sh.part_mass[p], (u64)__builtin_rint((double)s * sh.factor[p]));
         }
         __syncthreads();
         if (wave == 0) {
@@ -944,7 +947,7 @@ template <typename T> __global__ __launch_bounds__(kPartThreads) void probs_kern
         for (int i = lo + threadIdx.x; i < hi; i += kPartThreads) probs[i] = c.kind == kLargest && i == c.at ? 1.f : 0.f;
         return;
     }
-    fill_roots(root);
+    fill_roots(root, bits);
     __syncthreads();
     const Row row = row_at(c.top, a.temperature ? a.temperature[n] : 1.f, bits, root);
     const double f = 1.0 / (double)c.total;
@@ -956,10 +959,10 @@ template <typename T> __global__ __launch_bounds__(kPartThreads) void probs_kern
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Parts of a row: enough workgroups for the chip, of 2048 logits or more; of
+// Parts of a row: enough workgroups for the chip, of 4096 logits or more; of
 // 8192 at most, as the token's part is gone through again by one workgroup.
 void lay_out(Work &w, int rows, int vocab, void *workspace, size_t &bytes) {
-    const long most = std::min<long>(kMostParts, (vocab + 2047) / 2048);
+    const long most = std::min<long>(kMostParts, (vocab + 4095) / 4096);
     w.parts = (int)std::max<long>(1, std::min<long>(most, std::max<long>((1024 + rows - 1) / rows, vocab / 8192)));
     w.length = ((vocab + w.parts - 1) / w.parts + 7) / 8 * 8;
     w.parts = (vocab + w.length - 1) / w.length;
