@@ -35,7 +35,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves, kTile = 64;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr float kNone = -1e30f;   // a reference below every score
 
 // How a call is laid out over the chip.  Columns of a workgroup: SPLIT kernels
@@ -43,6 +43,7 @@ constexpr float kNone = -1e30f;   // a reference below every score
 // the others each wave 16 NT of its own.
 struct Layout {
     int nt;
+    int keys;        // of a tile
     bool split;
     int cols;        // of a workgroup
     long units;      // (request, columns) pairs, at most
@@ -54,23 +55,26 @@ Layout layout_of(int num_seqs, int total_tokens, int q_heads, int heads, bool io
     const long g = q_heads / heads, columns = (long)total_tokens * g, each = num_seqs ? (columns + num_seqs - 1) / num_seqs : 0;
     y.nt = each <= 16 ? 1 : each <= 32 || !io_bf16 ? 2 : 4;
     y.split = each <= 32;
+    y.keys = y.split ? 64 : 32;
     y.cols = 16 * y.nt * (y.split ? 1 : kWaves);
     y.units = columns / y.cols + num_seqs;
     long more = 0;
-    if (y.split) more = std::max<long>((1536 + heads - 1) / heads, y.units / 4);
+    if (y.split) more = std::max<long>((768 + heads - 1) / heads, y.units / 4);
     else if (y.units * heads < 512) more = (1024 + heads - 1) / heads;
     y.places = y.units + more;
+    static_assert(16 * 4 * kWaves <= 256, "a column's number has 8 bits");
     return y;
 }
 
 struct Plan {
     int units, places, least;   // least: tiles of a chunk
-    int *info;                  // [0]: chunk length; then first place and chunks of every request
+    int *info;                  // [tokens, query heads, 2]: place of a column's first chunk; how many it has, and the
+                                // column's number there in the low 8 bits
     float *sums;                // [places, heads, cols, 2]: m, l
     float *parts;               // [places, heads, cols, d]
 };
 
-size_t info_bytes(int num_seqs) { return ((size_t)num_seqs * 8 + 16 + 255) / 256 * 256; }
+size_t info_bytes(long columns) { return ((size_t)columns * 8 + 255) / 256 * 256; }
 
 __device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
 #pragma unroll
@@ -85,7 +89,7 @@ __device__ __forceinline__ unsigned long long wave_sum(unsigned long long x) {
 
 struct Request { int begin, length, total, units, tiles; };
 
-__device__ __forceinline__ Request request_of(const AttendArgs &a, int n, int g, int cols) {
+__device__ __forceinline__ Request request_of(const AttendArgs &a, int n, int g, int cols, int keys) {
     Request r;
     r.begin = max(a.cu_seqlens[n], 0);
     r.length = max(min(a.cu_seqlens[n + 1], a.total_tokens) - r.begin, 0);
@@ -93,7 +97,7 @@ __device__ __forceinline__ Request request_of(const AttendArgs &a, int n, int g,
     const long most = (long)a.max_blocks << a.block_shift;
     r.total = (unsigned)row < (unsigned)a.rows ? (int)min((long)max(a.kv_totals[n], 0), most) : 0;
     r.units = (int)(((long)r.length * g + cols - 1) / cols);
-    r.tiles = (int)(((long)r.total + kTile - 1) / kTile);
+    r.tiles = (int)(((long)r.total + keys - 1) / keys);
     return r;
 }
 
@@ -102,7 +106,7 @@ struct Unit { int n, column, chunk, chunks, length; };   // column: index of the
 // What place p stands for (n < 0: nothing).  Every workgroup finds it by itself
 // from the lengths, which takes a microsecond for some hundred requests; a
 // launch before this one would take four.
-__device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int cols, bool tell) {
+__device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int cols, int keys) {
     __shared__ unsigned long long work[kWaves];
     __shared__ uint32_t part[kWaves];
     __shared__ int found[4];
@@ -111,7 +115,7 @@ __device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int
     if (plan.places > plan.units) {
         unsigned long long w = 0;
         for (int n = tid; n < a.num_seqs; n += kThreads) {
-            const Request r = request_of(a, n, g, cols);
+            const Request r = request_of(a, n, g, cols, keys);
             w += (unsigned long long)r.units * r.tiles;
         }
         w = wave_sum(w);
@@ -129,7 +133,7 @@ __device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int
         uint32_t take = 0;
         int chunks = 1;
         if (n < a.num_seqs) {
-            const Request r = request_of(a, n, g, cols);
+            const Request r = request_of(a, n, g, cols, keys);
             chunks = max(1, (r.tiles + u.length - 1) / u.length);
             take = (uint32_t)r.units * chunks;
         }
@@ -148,10 +152,6 @@ __device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int
             if (w < wave) incl += part[w];
             all += part[w];
         }
-        if (tell && n < a.num_seqs) {
-            plan.info[4 + 2 * n] = (int)(incl - take);
-            plan.info[5 + 2 * n] = chunks;
-        }
         if ((uint32_t)p < incl && (uint32_t)p >= incl - take) {
             found[0] = n;
             found[1] = (int)(p - (incl - take)) / chunks;
@@ -160,9 +160,8 @@ __device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int
         }
         before += all;
         __syncthreads();
-        if (!tell && before > (uint32_t)p) break;
+        if (before > (uint32_t)p) break;
     }
-    if (tell && tid == 0) plan.info[0] = u.length;
     u.n = found[0];
     u.column = found[1];
     u.chunk = found[2];
@@ -192,33 +191,66 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) { return __bui
 // Bytes of w that are NaN, as 0x80 in each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-template <typename T, int D, int NT, bool SPLIT>
-__global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const AttendArgs a, const Plan plan) {
+// Max over the four lane groups, in every lane.
+__device__ __forceinline__ float group_max(float x) {
+    const uint32_t b = __float_as_uint(x);
+    const auto p = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    x = __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const uint32_t c = __float_as_uint(x);
+    const auto q = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+    return __builtin_fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+template <int N> struct Bytes;   // of one lane's share of a row of values
+template <> struct Bytes<16> { u32x4 w; };
+template <> struct Bytes<8> { u32x2 w; };
+
+// KEYS keys a step.  64 take 16 bytes a lane of keys and of values; 32 leave room
+// for twice the columns in the registers of two waves a SIMD, whose matrix and
+// vector instructions then overlap, with the queries in LDS.
+template <typename T, int D, int NT, int KEYS, bool SPLIT>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void attend_kernel(const AttendArgs a, const Plan plan) {
     constexpr int TERMS = sizeof(T) == 4 ? 3 : 1, KL = D / 64, MT = D / 16, WAVE = 16 * NT, COLS = SPLIT ? WAVE : kWaves * WAVE;
-    __shared__ float joined[kWaves][4][256];
+    constexpr int ST = KEYS / 16, PS = KEYS / 32, OWN = KEYS / 4;   // score tiles, product steps, keys of a lane group
+    constexpr bool QLDS = !SPLIT;
+    constexpr int QBYTES = QLDS ? kWaves * NT * KL * 2 * TERMS * 1024 : 16, JOIN = kWaves * 4 * 256 * 4;
+    __shared__ __align__(16) unsigned char pool[QBYTES > JOIN ? QBYTES : JOIN];   // the queries, then the waves' sums
     __shared__ float stats[kWaves][WAVE][2];
+    float (*joined)[4][256] = reinterpret_cast<float (*)[4][256]>(pool);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, grp = lane >> 4;
     const int head = blockIdx.x % a.heads, place = blockIdx.x / a.heads, g = a.q_heads / a.heads;
-    const Unit u = unit_of(a, plan, place, g, COLS, place == 0 && head == 0 && plan.places > plan.units);
+    const Unit u = unit_of(a, plan, place, g, COLS, KEYS);
     if (u.n < 0) return;
-    const Request r = request_of(a, u.n, g, COLS);
+    const Request r = request_of(a, u.n, g, COLS, KEYS);
     // the last columns first: they see the most keys
     const int all = r.length * g, first = (r.units - 1 - u.column) * COLS, end = min(first + COLS, all);
     const int before = r.total - r.length;                                // position of the request's first token
     const int unit_keys = max(before + (end - 1) / g + 1, 0);
-    const int unit_tiles = (unit_keys + kTile - 1) / kTile;
+    const int unit_tiles = (unit_keys + KEYS - 1) / KEYS;
     const int chunks = max(1, (unit_tiles + u.length - 1) / u.length);    // that this unit really has
     if (u.chunk >= chunks) return;
+    if (plan.places > plan.units && u.chunk == 0)                         // for the launch that joins the chunks
+        for (int col = first + threadIdx.x; col < end; col += kThreads) {
+            const int token = col / g;
+            int *to = plan.info + 2 * ((long)(r.begin + token) * a.q_heads + (long)head * g + (col - token * g));
+            to[0] = place;
+            to[1] = chunks << 8 | (col - first);
+        }
     const bool same = SPLIT || end - first <= WAVE;                       // the waves share columns and split the keys
     const int col0 = first + (same ? 0 : wave * WAVE), col1 = min(col0 + WAVE, end);
     const int seen = col1 > col0 ? max(before + (col1 - 1) / g + 1, 0) : 0;   // keys that some column of this wave sees
     const int least = col1 > col0 ? before + col0 / g : -1;                   // the last key that all of them see
     const int step = same ? kWaves : 1;
-    const int stop = min((u.chunk + 1) * u.length, (seen + kTile - 1) / kTile);
+    const int stop = min((u.chunk + 1) * u.length, (seen + KEYS - 1) / KEYS);
     int tile = u.chunk * u.length + (same ? wave : 0);
 
     // queries
-    bf16x8 q[NT][KL][2][TERMS];
+    bf16x8 qreg[QLDS ? 1 : NT][KL][2][TERMS];
+    bf16x8 *qlds = reinterpret_cast<bf16x8 *>(pool) + wave * (NT * KL * 2 * TERMS * 64) + lane;
+    const auto query = [&](int nt, int j, int h, int i) {
+        if constexpr (QLDS) return qlds[(((nt * KL + j) * 2 + h) * TERMS + i) * 64];
+        else return qreg[nt][j][h][i];
+    };
     int last[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -232,10 +264,11 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const T *at = src + 64 * j + 16 * grp + 8 * s;
+                bf16x8 t[TERMS];
                 if constexpr (TERMS == 1) {
                     u32x4 w{0, 0, 0, 0};
                     if (in) w = *reinterpret_cast<const u32x4 *>(at);
-                    q[nt][j][s][0] = __builtin_bit_cast(bf16x8, w);
+                    t[0] = __builtin_bit_cast(bf16x8, w);
                 } else {
                     f32x4 x{0.f, 0.f, 0.f, 0.f}, y{0.f, 0.f, 0.f, 0.f};
                     if (in) {
@@ -244,9 +277,14 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        terms_of<TERMS>(x[e], e, q[nt][j][s]);
-                        terms_of<TERMS>(y[e], 4 + e, q[nt][j][s]);
+                        terms_of<TERMS>(x[e], e, t);
+                        terms_of<TERMS>(y[e], 4 + e, t);
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) {
+                    if constexpr (QLDS) qlds[(((nt * KL + j) * 2 + s) * TERMS + i) * 64] = t[i];
+                    else qreg[nt][j][s][i] = t[i];
                 }
             }
     }
@@ -255,30 +293,31 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
     const int32_t *table = a.block_table + (long)a.indices[u.n] * a.max_blocks;
     const float to2 = a.scale * kLog2e;
     const auto page = [&](int tile, int group) {
-        const int i = (tile * kTile + 16 * group) >> a.block_shift;
+        const int i = (tile * KEYS + OWN * group) >> a.block_shift;
         return table[min(i, a.max_blocks - 1)];
     };
-    u32x4 kr[4][KL], vr[MT];
+    u32x4 kr[ST][KL];
+    Bytes<OWN> vr[MT];
     float ks, vs;
-    bool fine;   // this lane's sixteen keys begin in a block that holds some
+    bool fine;   // this lane's keys begin in a block that holds some
     const auto load_k = [&](int tile, int block) {
-        const int b = (unsigned)block < (unsigned)a.num_blocks ? block : 0, off = (tile * kTile + 16 * (c >> 2)) & within;
+        const int b = (unsigned)block < (unsigned)a.num_blocks ? block : 0, off = (tile * KEYS + OWN * (c >> 2)) & within;
         const long at = (long)b * a.heads + head;
         ks = a.k_scale[at];
         const uint8_t *p = a.k_cache + (at * bs + off + (c & 3)) * D + 16 * grp;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < ST; ++t)
 #pragma unroll
             for (int j = 0; j < KL; ++j) kr[t][j] = *reinterpret_cast<const u32x4 *>(p + 4 * t * D + 64 * j);
     };
     const auto load_v = [&](int tile, int block) {
-        fine = (unsigned)block < (unsigned)a.num_blocks && tile * kTile + 16 * grp < r.total;
-        const int b = fine ? block : 0, off = (tile * kTile + 16 * grp) & within;
+        fine = (unsigned)block < (unsigned)a.num_blocks && tile * KEYS + OWN * grp < r.total;
+        const int b = fine ? block : 0, off = (tile * KEYS + OWN * grp) & within;
         const long at = (long)b * a.heads + head;
         vs = fine ? a.v_scale[at] : 1.f;
         const uint8_t *p = a.v_cache + (at * D + c) * bs + off;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) vr[t] = *reinterpret_cast<const u32x4 *>(p + 16 * t * bs);
+        for (int t = 0; t < MT; ++t) vr[t] = *reinterpret_cast<const Bytes<OWN> *>(p + 16 * t * bs);
     };
 
     f32x4 o[MT][NT];
@@ -298,33 +337,38 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
     for (; tile < stop; tile += step) {
         const int next = min(tile + step, stop - 1);   // the last one is loaded again, unused
         const int kpage = page(next, c >> 2), vpage = page(next, grp);
-        f32x4 s[4][NT];
+        f32x4 s[ST][NT];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < ST; ++t)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) s[t][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int j = 0; j < KL; ++j)
 #pragma unroll
-            for (int j = 0; j < KL; ++j)
+            for (int h = 0; h < 2; ++h) {
+                bf16x8 k[ST];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bf16x8 k = widen(kr[t][j][2 * h], kr[t][j][2 * h + 1], ks);
+                for (int t = 0; t < ST; ++t) k[t] = widen(kr[t][j][2 * h], kr[t][j][2 * h + 1], ks);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = TERMS - 1; i >= 0; --i) s[t][nt] = mma(k, q[nt][j][h][i], s[t][nt]);
-                }
+                    for (int i = TERMS - 1; i >= 0; --i) {
+                        const bf16x8 q = query(nt, j, h, i);
+#pragma unroll
+                        for (int t = 0; t < ST; ++t) s[t][nt] = mma(k[t], q, s[t][nt]);
+                    }
+            }
         load_k(next, kpage);
-        const bool masked = tile * kTile + kTile - 1 > least || __any(!fine);
+        const bool masked = tile * KEYS + KEYS - 1 > least || __any(!fine);
         if (masked) {
+            asm volatile("");   // a branch: most tiles have nothing to hide
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (!fine || tile * kTile + 16 * grp + 4 * t + i > last[nt]) s[t][nt][i] = -__builtin_inff();
+                        if (!fine || tile * KEYS + OWN * grp + 4 * t + i > last[nt]) s[t][nt][i] = -__builtin_inff();
         }
         // a reference that holds until a score passes it by 2^8
         float top[NT];
@@ -333,15 +377,15 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
         for (int nt = 0; nt < NT; ++nt) {
             float x = s[0][nt][0];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x = __builtin_fmaxf(x, s[t][nt][i]);
-            x = __builtin_fmaxf(x, __shfl_xor(x, 16, 64));
-            x = __builtin_fmaxf(x, __shfl_xor(x, 32, 64));
+            x = group_max(x);
             top[nt] = x;
             raise |= (x - m[nt]) * to2 > 8.f;
         }
         if (__any(raise)) {
+            asm volatile("");
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float to = __builtin_fmaxf(m[nt], top[nt]), f = __builtin_amdgcn_exp2f((m[nt] - to) * to2);
@@ -353,12 +397,12 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
                     for (int i = 0; i < 4; ++i) o[t][nt][i] *= f;
             }
         }
-        bf16x8 p[NT][2][TERMS];
+        bf16x8 p[NT][PS][TERMS];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float shift = -m[nt] * to2;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][nt][i], to2, shift));
@@ -367,52 +411,50 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
                 }
         }
         if (masked) {
+            asm volatile("");
             // what a column must not see may be NaN, and 0 * NaN would reach it
             uint32_t bad = 0;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) bad |= nan_bytes(vr[t][i]);
+                for (int i = 0; i < OWN / 4; ++i) bad |= nan_bytes(vr[t].w[i]);
             if (__any(bad != 0)) {
-                bf16x8 one[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            one[nt][h][e] = (__bf16)(!fine || tile * kTile + 16 * grp + 8 * h + e > last[nt] ? 0.f : 1.f);
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    f32x4 hit[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) hit[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    u32x4 flag;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t b = nan_bytes(vr[t][i]) >> 7;
-                        vr[t][i] &= ~(b * 0xffu);
-                        flag[i] = b * 0x38u;   // e4m3's one
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const bf16x8 f = widen(flag[2 * h], flag[2 * h + 1], 1.f);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) hit[nt] = mma(f, one[nt][h], hit[nt]);
-                    }
+                asm volatile("");
+                // the NaN among the values become zeros here, and NaN in the columns that see them
+#pragma unroll 1
+                for (int h = 0; h < PS; ++h) {
+                    bf16x8 one[NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (hit[nt][i] > 0.f) o[t][nt][i] = __builtin_nanf("");
+                        for (int e = 0; e < 8; ++e)
+                            one[nt][e] = (__bf16)(!fine || tile * KEYS + OWN * grp + 8 * h + e > last[nt] ? 0.f : 1.f);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        uint32_t flag[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) flag[i] = (nan_bytes(PS == 1 || h == 0 ? vr[t].w[i] : vr[t].w[OWN / 4 - 2 + i]) >> 7) * 0x38u;   // e4m3's one
+                        const bf16x8 f = widen(flag[0], flag[1], 1.f);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const f32x4 hit = mma(f, one[nt], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (hit[i] > 0.f) o[t][nt][i] = __builtin_nanf("");
+                        }
+                    }
                 }
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < OWN / 4; ++i) vr[t].w[i] &= ~((nan_bytes(vr[t].w[i]) >> 7) * 0xffu);
             }
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bf16x8 v = widen(vr[t][2 * h], vr[t][2 * h + 1], vs);
+            for (int h = 0; h < PS; ++h) {
+                const bf16x8 v = widen(vr[t].w[2 * h], vr[t].w[2 * h + 1], vs);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -461,7 +503,7 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
             stats[wave][16 * nt + c][0] = m[nt];
             stats[wave][16 * nt + c][1] = l[nt];
         }
-    __syncthreads();
+    __syncthreads();   // and no wave needs its queries any more
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float to = kNone, sum = 0.f;
@@ -493,36 +535,20 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 1 : 2) void attend_kernel(const
 
 // The chunks of a column (token, query head) joined; one wave a column.
 template <typename T, int D> __global__ __launch_bounds__(256) void join_kernel(const AttendArgs a, const Plan plan, int cols) {
-    const int lane = threadIdx.x & 63, g = a.q_heads / a.heads;
+    const int lane = threadIdx.x & 63;
     const long column = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int token = (int)(column / a.q_heads), qh = (int)(column % a.q_heads), head = qh / g;
-    if (token >= a.total_tokens) return;
-    int lo = 0, num = a.num_seqs;
-    while (num > 1) {
-        const int half = num >> 1;
-        if (a.cu_seqlens[lo + half] <= token) {
-            lo += half;
-            num -= half;
-        } else {
-            num = half;
-        }
-    }
-    const Request r = request_of(a, lo, g, cols);
-    if (token < r.begin || token - r.begin >= r.length) return;
-    const int col = (token - r.begin) * g + (qh - head * g), ct = col / cols, length = plan.info[0];
-    const int end = min((ct + 1) * cols, r.length * g);
-    const int keys = max(r.total - r.length + (end - 1) / g + 1, 0), tiles = (keys + kTile - 1) / kTile;
-    const int chunks = max(1, (tiles + length - 1) / length);
-    if (chunks == 1) return;
-    const long place = plan.info[4 + 2 * lo] + (long)(r.units - 1 - ct) * plan.info[5 + 2 * lo];
-    if (place + chunks > plan.places) return;   // offsets that do not fit the call
+    const int token = (int)(column / a.q_heads), head = (int)(column % a.q_heads) / (a.q_heads / a.heads);
+    if (token >= min(a.cu_seqlens[a.num_seqs], a.total_tokens)) return;
+    const uint32_t place = (uint32_t)plan.info[2 * column], chunks = (uint32_t)plan.info[2 * column + 1] >> 8;
+    const int col = plan.info[2 * column + 1] & 0xff;
+    if (chunks == 1 || (long)place + chunks > plan.places) return;   // (never more than there are, if the offsets fit the call)
     const float to2 = a.scale * kLog2e;
-    const auto at = [&](int k) { return ((place + k) * a.heads + head) * cols + col - ct * cols; };
+    const auto at = [&](int k) { return ((long)(place + k) * a.heads + head) * cols + col; };
     float top = kNone, sum = 0.f, x[D / 64];
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) x[i] = 0.f;
-    for (int k0 = 0; k0 < chunks; k0 += 64) {   // a chunk a lane
-        const int some = min(chunks - k0, 64);
+    for (int k0 = 0; k0 < (int)chunks; k0 += 64) {   // a chunk a lane
+        const int some = min((int)chunks - k0, 64);
         f32x2 ml{kNone, 0.f};
         if (lane < some) ml = *reinterpret_cast<const f32x2 *>(plan.sums + at(k0 + lane) * 2);
         float m = ml[0];
@@ -533,11 +559,20 @@ template <typename T, int D> __global__ __launch_bounds__(256) void join_kernel(
         sum = sum * again + group_sum<64>(f * ml[1]);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) x[i] *= again;
-#pragma unroll 8
-        for (int k = 0; k < some; ++k) {
-            const float g = __shfl(f, k, 64);
+        constexpr int AHEAD = 8;
+        for (int k = 0; k < some; k += AHEAD) {
+            float y[AHEAD][D / 64];
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) x[i] += g * plan.parts[at(k0 + k) * D + lane + 64 * i];
+            for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) y[e][i] = plan.parts[at(k0 + min(k + e, some - 1)) * D + lane + 64 * i];
+#pragma unroll
+            for (int e = 0; e < AHEAD; ++e) {
+                const float g = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), min(k + e, 63)));
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    if (k + e < some) x[i] += g * y[e][i];
+            }
         }
     }
     T *to = static_cast<T *>(a.o) + column * D;
@@ -546,9 +581,9 @@ template <typename T, int D> __global__ __launch_bounds__(256) void join_kernel(
     for (int i = 0; i < D / 64; ++i) io_traits<T>::store(to, lane + 64 * i, x[i] * f);
 }
 
-template <typename T, int D, int NT, bool SPLIT>
+template <typename T, int D, int NT, int KEYS, bool SPLIT>
 hipError_t launch(const AttendArgs &a, const Layout &y, const Plan &plan, hipStream_t stream) {
-    attend_kernel<T, D, NT, SPLIT><<<(unsigned)(plan.places * a.heads), kThreads, 0, stream>>>(a, plan);
+    attend_kernel<T, D, NT, KEYS, SPLIT><<<(unsigned)(plan.places * a.heads), kThreads, 0, stream>>>(a, plan);
     if (plan.places > plan.units) {
         const long columns = (long)a.total_tokens * a.q_heads;
         join_kernel<T, D><<<(unsigned)((columns + 3) / 4), 256, 0, stream>>>(a, plan, y.cols);
@@ -557,9 +592,9 @@ hipError_t launch(const AttendArgs &a, const Layout &y, const Plan &plan, hipStr
 }
 
 template <typename T, int D> hipError_t launch(const AttendArgs &a, const Layout &y, const Plan &plan, hipStream_t stream) {
-    if (y.split) return y.nt == 1 ? launch<T, D, 1, true>(a, y, plan, stream) : launch<T, D, 2, true>(a, y, plan, stream);
-    if constexpr (sizeof(T) == 4) return launch<T, D, 2, false>(a, y, plan, stream);
-    else return launch<T, D, 4, false>(a, y, plan, stream);
+    if (y.split) return y.nt == 1 ? launch<T, D, 1, 64, true>(a, y, plan, stream) : launch<T, D, 2, 64, true>(a, y, plan, stream);
+    if constexpr (sizeof(T) == 4) return launch<T, D, 2, 32, false>(a, y, plan, stream);
+    else return launch<T, D, 4, 32, false>(a, y, plan, stream);
 }
 
 }  // namespace
@@ -567,7 +602,7 @@ template <typename T, int D> hipError_t launch(const AttendArgs &a, const Layout
 size_t attend_workspace_bytes(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16) {
     const Layout y = layout_of(num_seqs, total_tokens, q_heads, heads, io_bf16);
     if (y.places == y.units) return 0;
-    return info_bytes(num_seqs) + (size_t)y.places * heads * y.cols * (d + 2) * sizeof(float);
+    return info_bytes((long)total_tokens * q_heads) + (size_t)y.places * heads * y.cols * (d + 2) * sizeof(float);
 }
 
 long attend_grid(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16) {
@@ -580,9 +615,9 @@ hipError_t launch_attend(const AttendArgs &a, void *workspace, hipStream_t strea
     Plan plan{};
     plan.units = (int)y.units;
     plan.places = (int)y.places;
-    plan.least = y.split ? kWaves : 8;
+    plan.least = 512 / y.keys;
     plan.info = static_cast<int *>(workspace);
-    plan.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + info_bytes(a.num_seqs));
+    plan.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + info_bytes((long)a.total_tokens * a.q_heads));
     plan.sums = plan.parts + (size_t)y.places * a.heads * y.cols * a.d;
     if (a.io_bf16) return a.d == 64 ? launch<bf16, 64>(a, y, plan, stream) : launch<bf16, 128>(a, y, plan, stream);
     return a.d == 64 ? launch<float, 64>(a, y, plan, stream) : launch<float, 128>(a, y, plan, stream);
