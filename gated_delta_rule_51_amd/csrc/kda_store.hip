@@ -119,8 +119,10 @@ constexpr int kShort = 4;
 template <typename T, int D>
 __device__ __forceinline__ void store_short(const StoreArgs &a, int first, int f, int m, int block, int unit0, int units) {
     constexpr int N = Wide<T>::N, LPR = D / N;
-    const int c = threadIdx.x % LPR, shift = a.block_shift;
-    const int unit = unit0 + threadIdx.x / LPR;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int c = tid % LPR, shift = a.block_shift;
+    const int unit = unit0 + tid / LPR;
     if (unit >= units) return;
     const bool values = unit >= a.heads;
     const int h = values ? unit - a.heads : unit;
@@ -165,7 +167,9 @@ template <typename T, int D, bool VALUES>
 __device__ __forceinline__ void store_run(const T *x, long stride, uint8_t *cache, float *scale, int f, int m, int shift,
                                           uint8_t *tile, float *most) {
     constexpr int N = Wide<T>::N, LPR = D / N, RPP = 4 * kThreads / LPR;
-    const int tid = threadIdx.x, c = tid % LPR, r0 = 4 * (tid / LPR);
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));   // addresses are formed here, not kept from before the loops around this
+    const int c = tid % LPR, r0 = 4 * (tid / LPR);
     Wide<T> held[4];   // the first rows stay in registers, any others are read again
     float top = 0.f;
     const auto load = [&](int r) { return Wide<T>{*reinterpret_cast<const u32x4 *>(x + (long)min(r, m - 1) * stride + c * N)}; };
@@ -231,7 +235,7 @@ __device__ __forceinline__ void store_run(const T *x, long stride, uint8_t *cach
 // The runs that begin among R <= 128 tokens; of their 2 H rows (H of keys, then H
 // of values) those of this workgroup's turn.  Turns, not tokens, lie far apart:
 // where runs are short the first turn does it all and the others only end.
-template <typename T, int D> __global__ __launch_bounds__(kThreads) void store_kernel(const StoreArgs a, int R, int turns) {
+template <typename T, int D> __global__ __launch_bounds__(kThreads, 8) void store_kernel(const StoreArgs a, int R, int turns) {
     __shared__ __align__(16) uint8_t tile[D * 128];
     __shared__ float most[4];
     constexpr int LPR = D / Wide<T>::N, AT_ONCE = kThreads / LPR;
