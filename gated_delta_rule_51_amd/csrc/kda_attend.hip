@@ -615,7 +615,7 @@ hipError_t launch_attend(const AttendArgs &a, void *workspace, hipStream_t strea
     Plan plan{};
     plan.units = (int)y.units;
     plan.places = (int)y.places;
-    plan.least = 512 / y.keys;
+    plan.least = y.split ? 8 : 4;   // two tiles a wave; four
     plan.info = static_cast<int *>(workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + info_bytes((long)a.total_tokens * a.q_heads));
     plan.sums = plan.parts + (size_t)y.places * a.heads * y.cols * a.d;
