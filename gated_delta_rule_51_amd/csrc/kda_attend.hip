@@ -370,7 +370,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
                     for (int i = 0; i < 4; ++i)
                         if (!fine || tile * KEYS + OWN * grp + 4 * t + i > last[nt]) s[t][nt][i] = -__builtin_inff();
         }
-        // a reference that holds until a score passes it by 2^8
+        // A reference that holds until a score passes it by 2^8; whether one does is
+        // asked of every lane's own scores, and the column's largest sought only then.
         float top[NT];
         bool raise = false;
 #pragma unroll
@@ -380,7 +381,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
             for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x = __builtin_fmaxf(x, s[t][nt][i]);
-            x = group_max(x);
             top[nt] = x;
             raise |= (x - m[nt]) * to2 > 8.f;
         }
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
             asm volatile("");
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float to = __builtin_fmaxf(m[nt], top[nt]), f = __builtin_amdgcn_exp2f((m[nt] - to) * to2);
+                const float to = __builtin_fmaxf(m[nt], group_max(top[nt])), f = __builtin_amdgcn_exp2f((m[nt] - to) * to2);
                 m[nt] = to;
                 l[nt] *= f;
 #pragma unroll
@@ -404,10 +404,20 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
 #pragma unroll
             for (int t = 0; t < ST; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; i += 2) {
                     const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][nt][i], to2, shift));
-                    l[nt] += x;
-                    terms_of<TERMS>(x, 4 * (t & 1) + i, p[nt][t >> 1]);
+                    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][nt][i + 1], to2, shift));
+                    if constexpr (TERMS == 1) {   // the sum of what the product sees, two at a time
+                        const bf16x2 z{(__bf16)x, (__bf16)y};
+                        p[nt][t >> 1][0][4 * (t & 1) + i] = z[0];
+                        p[nt][t >> 1][0][4 * (t & 1) + i + 1] = z[1];
+                        l[nt] = __builtin_amdgcn_fdot2_f32_bf16(z, bf16x2{(__bf16)1.f, (__bf16)1.f}, l[nt], false);
+                    } else {
+                        l[nt] += x;
+                        l[nt] += y;
+                        terms_of<TERMS>(x, 4 * (t & 1) + i, p[nt][t >> 1]);
+                        terms_of<TERMS>(y, 4 * (t & 1) + i + 1, p[nt][t >> 1]);
+                    }
                 }
         }
         if (masked) {
