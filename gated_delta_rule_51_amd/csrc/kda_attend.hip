@@ -671,7 +671,13 @@ hipError_t launch_attend(const AttendArgs &a, void *workspace, hipStream_t strea
     Plan plan{};
     plan.units = (int)y.units;
     plan.places = (int)y.places;
-    plan.least = y.split ? 8 : 4;   // two tiles a wave; four
+    // Tiles of a chunk at least.  Single tokens: two for each of the four waves (one
+    // request of 8000 tokens 14 us, with one 20).  Prompts: a chunk's sums of all its
+    // columns are written and read once more, 128 KB for 256 columns of 128 channels, so
+    // 512 keys (6 prompts of up to 409 tokens, 200 workgroups: 28 us, with 128 keys 46),
+    // but 128 where the undivided columns are no 96 workgroups (one of 1889 tokens over
+    // 2 heads, 30 workgroups: 21 us, with 512 keys 27).
+    plan.least = y.split ? 8 : y.units * a.heads < 96 ? 4 : a.io_bf16 ? 16 : 8;
     plan.info = static_cast<int *>(workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + info_bytes((long)a.total_tokens * a.q_heads));
     plan.sums = plan.parts + (size_t)y.places * a.heads * y.cols * a.d;
