@@ -311,7 +311,7 @@ const char *kda_status_string(kda_status s) {
     return "unknown status";
 }
 
-int32_t kda_version(void) { return 300; }
+int32_t kda_version(void) { return 400; }
 
 size_t kda_chunk_prefill_workspace_size(const kda_prefill_desc *d) {
     if (check_desc(d) != KDA_OK) return 0;

@@ -162,6 +162,7 @@ struct SampleArgs {
     long stride;
 };
 size_t sample_workspace_bytes(int rows, int vocab);
+bool sample_fits(int rows, int vocab);   // its grids within the device's limits
 hipError_t launch_sample(const SampleArgs &a, void *workspace, hipStream_t stream);
 
 }  // namespace kda

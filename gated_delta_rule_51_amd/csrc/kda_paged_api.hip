@@ -82,7 +82,7 @@ kda_status check_sample(const kda_sample_desc *d) {
     if (!d) return KDA_ERR_NULL;
     if (d->num_rows < 0 || d->vocab <= 0 || d->stride < d->vocab) return KDA_ERR_SHAPE;
     if (!dtype_ok(d->logits_dtype) || d->vocab > (1 << 20)) return KDA_ERR_UNSUPPORTED;
-    return KDA_OK;
+    return d->num_rows == 0 || sample_fits(d->num_rows, d->vocab) ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
 
 }  // namespace

@@ -995,6 +995,13 @@ size_t sample_workspace_bytes(int rows, int vocab) {
     return bytes;
 }
 
+bool sample_fits(int rows, int vocab) {
+    Work w{};
+    size_t bytes = 0;
+    lay_out(w, rows, vocab, nullptr, bytes);
+    return (size_t)rows <= UINT32_MAX / kThreads && (size_t)rows * w.parts <= UINT32_MAX / kPartThreads;
+}
+
 hipError_t launch_sample(const SampleArgs &a, void *workspace, hipStream_t stream) {
     const int index_bits = 32 - __builtin_clz((unsigned)(a.vocab > 1 ? a.vocab - 1 : 1));
     const int bits = index_bits <= 16 ? 46 : 62 - index_bits;

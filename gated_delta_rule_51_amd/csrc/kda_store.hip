@@ -299,7 +299,9 @@ hipError_t launch_kv_store(const StoreArgs &a, hipStream_t stream) {
     // rows: one of them stores a single token, so few of few tokens.
     int R = 1;
     while (R < (1 << a.block_shift) && (long)a.total_tokens * a.heads / R > 4096) R *= 2;
-    const int turns = std::min(a.total_tokens <= 2048 ? 4 : 65535, 2 * a.heads);
+    const long tiles = ((long)a.total_tokens + R - 1) / R, most = UINT32_MAX / kThreads / std::max(tiles, 1l);   // a grid's threads are 32 bits
+    if (most < 1) return hipErrorInvalidConfiguration;
+    const int turns = (int)std::min<long>({a.total_tokens <= 2048 ? 4 : 65535, 2l * a.heads, most});
     if (a.io_bf16) return a.d == 64 ? launch<bf16, 64>(a, R, turns, stream) : launch<bf16, 128>(a, R, turns, stream);
     return a.d == 64 ? launch<float, 64>(a, R, turns, stream) : launch<float, 128>(a, R, turns, stream);
 }

@@ -663,10 +663,11 @@ kda_status kda_kv_store(const kda_kv_desc *desc, const void *k, const void *v, c
  *              written; must not overlap any input
  * Precision: keys and values are exact in bf16, the matrix cores' operands.  bf16
  * queries are operands as they are, and softmax's numerators are rounded to bf16
- * (2^-8 of each) for the second product; with fp32 io queries and numerators go
- * in as the sum of three bf16 terms, which hold all their bits.  Scores, sums and
- * outputs accumulate in fp32.  What a token does not see has no part in its
- * output, NaN or not.
+ * (2^-8 of each) for the second product and for their sum alike; with fp32 io
+ * queries and numerators go in as the sum of three bf16 terms, which hold all
+ * their bits.  Scores, sums and outputs accumulate in fp32.  What a token does not
+ * see has no part in its output, NaN or not.  Not checked: scores lie within
+ * +-10^30.  Calls of the same sizes and lengths add in the same order.
  * The workspace overlaps nothing else; it may be reused by calls that are ordered
  * on one stream.  T * Hq < 2^31.
  */

@@ -8,9 +8,11 @@ accumulation may truncate).  A score is a sum of D exact products: it is off by
 subtracted is of that size too, and scaling, subtraction and the exponential's
 argument round three times, exp2 by one step: a numerator is off by
 ep = e ((D + 10) A + 8), relative.  fp32 io adds the operands' remainder after
-three bf16 terms, below e.  A rounding of numerators to bf16 adds 2^-8.  Sums over
-n keys add (n + 64) e to the numerators' sum and to the product's.  All of that
-goes with sum p |v| / sum p, and the output's own rounding with |o|.
+three bf16 terms, below e.  Numerators rounded to bf16, p_i (1 + d_i) with |d_i| <=
+2^-8, in the product and in its divisor alike move o by sum d_i p_i (v_i - o) / sum p
+to first order: at most 2^-8 (sum p |v| / sum p + |o|).  Sums over n keys add (n +
+64) e to the numerators' sum and to the product's.  All else goes with sum p |v| /
+sum p, and the output's own rounding with |o|.
 """
 import numpy as np
 import torch
@@ -154,6 +156,8 @@ def attention(q, cu, totals, idx, table, k_cache, v_cache, k_scale, v_scale, sca
                     ep = E32 * ((D + 10) * A + 8)
                     near = 2 * ep + (2.0 ** -8 if io == torch.bfloat16 else 4 * E32) + 2 * (len(see) + 64) * E32
                     tol[cu[n] + j, i] = near * (p @ np.abs(v[see])) / p.sum()
+                    if io == torch.bfloat16:
+                        tol[cu[n] + j, i] += 2.0 ** -8 * np.abs(o[cu[n] + j, i])
     return o, tol
 
 

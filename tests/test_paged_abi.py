@@ -152,7 +152,8 @@ def test_sample_refusals(L):  # noqa: F811
     run = lambda d, given: call(fn, d, SAMPLE, given, (need,))  # noqa: E731
     assert run(None, {}) == NULL
     for kw, want in ((dict(num_rows=-1), SHAPE), (dict(vocab=0), SHAPE), (dict(stride=999), SHAPE), (dict(logits_dtype=2), UNSUP),
-                     (dict(vocab=(1 << 20) + 1, stride=1 << 21), UNSUP)):
+                     (dict(vocab=(1 << 20) + 1, stride=1 << 21), UNSUP), (dict(num_rows=1 << 23), UNSUP),
+                     (dict(num_rows=1 << 20, vocab=1 << 20, stride=1 << 20), UNSUP)):
         assert run(make(**kw), {}) == want, kw
         assert L.kda_sample_tokens_workspace_size(ctypes.byref(make(**kw))) == 0
     assert run(d, {"x": None}) == NULL and run(d, {"u": None}) == NULL and run(d, {"tokens": None, "probs": None}) == NULL
