@@ -294,14 +294,19 @@ template <typename T, int D> hipError_t launch(const StoreArgs &a, int R, int tu
 }  // namespace
 
 hipError_t launch_kv_store(const StoreArgs &a, hipStream_t stream) {
-    // Tokens looked at by one workgroup: one of few tokens, each of which is
-    // likely to be a run, up to a block of many.  Workgroups that share a run's
-    // rows: one of them stores a single token, so few of few tokens.
+    // Workgroups that share a run's rows, in turns: a single token is stored by the
+    // first alone, so four where there are few tokens (295 tokens of runs up to 4 over
+    // 16 heads: 12 us, 13.6 with a turn for each row; 1637 tokens of 7 prompts: 24 and
+    // 18).  Tokens looked at by one workgroup: one of few, up to a block of many, as
+    // starting a workgroup costs what looking at a token does (1731 tokens over 2
+    // heads: 6.9 us with 4 tokens each, 13 with one).
+    const int some = std::min(a.total_tokens <= 512 ? 4 : 65535, 2 * a.heads);
     int R = 1;
-    while (R < (1 << a.block_shift) && (long)a.total_tokens * a.heads / R > 4096) R *= 2;
-    const long tiles = ((long)a.total_tokens + R - 1) / R, most = UINT32_MAX / kThreads / std::max(tiles, 1l);   // a grid's threads are 32 bits
+    const auto tiles = [&] { return ((long)a.total_tokens + R - 1) / R; };
+    while (R < (1 << a.block_shift) && (tiles() > 512 || tiles() * some > 4096)) R *= 2;
+    const long most = UINT32_MAX / kThreads / tiles();   // a grid's threads are 32 bits
     if (most < 1) return hipErrorInvalidConfiguration;
-    const int turns = (int)std::min<long>({a.total_tokens <= 2048 ? 4 : 65535, 2l * a.heads, most});
+    const int turns = (int)std::min<long>(some, most);
     if (a.io_bf16) return a.d == 64 ? launch<bf16, 64>(a, R, turns, stream) : launch<bf16, 128>(a, R, turns, stream);
     return a.d == 64 ? launch<float, 64>(a, R, turns, stream) : launch<float, 128>(a, R, turns, stream);
 }
