@@ -70,10 +70,16 @@ struct Plan {
     int units, places, least;   // least: tiles of a chunk
     int *info;                  // [tokens, query heads, 2]: place of a column's first chunk; how many it has, and the
                                 // column's number there in the low 8 bits
+    uint32_t *starts;           // [0]: chunk length; [1 + n]: first place of request n, the last: all places; or NULL
     float *sums;                // [places, heads, cols, 2]: m, l
     float *parts;               // [places, heads, cols, d]
 };
 
+// Up to this many requests every workgroup finds its place from the lengths by
+// itself, a request a thread, which takes about a microsecond; for more a launch
+// of one workgroup before them writes down where each request's places begin.
+constexpr int kFindOwn = kThreads;
+size_t starts_bytes(int num_seqs) { return num_seqs <= kFindOwn ? 0 : ((size_t)num_seqs * 4 + 8 + 255) / 256 * 256; }
 size_t info_bytes(long columns) { return ((size_t)columns * 8 + 255) / 256 * 256; }
 
 __device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
@@ -103,9 +109,83 @@ __device__ __forceinline__ Request request_of(const AttendArgs &a, int n, int g,
 
 struct Unit { int n, column, chunk, chunks, length; };   // column: index of the unit's columns; length: tiles of a chunk
 
-// What place p stands for (n < 0: nothing).  Every workgroup finds it by itself
-// from the lengths, which takes a microsecond for some hundred requests; a
-// launch before this one would take four.
+// Places of request r, and its chunks.
+__device__ __forceinline__ uint32_t places_of(const Request &r, int length, int &chunks) {
+    chunks = max(1, (r.tiles + length - 1) / length);
+    return (uint32_t)r.units * chunks;
+}
+
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(const AttendArgs a, const Plan plan, int cols, int keys) {
+    __shared__ unsigned long long work[kPlanWaves];
+    __shared__ uint32_t part[kPlanWaves];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = a.q_heads / a.heads;
+    int length = INT32_MAX / 2;
+    if (plan.places > plan.units) {
+        unsigned long long w = 0;
+        for (int n = tid; n < a.num_seqs; n += kPlanThreads) {
+            const Request r = request_of(a, n, g, cols, keys);
+            w += (unsigned long long)r.units * r.tiles;
+        }
+        w = wave_sum(w);
+        if (lane == 0) work[wave] = w;
+        __syncthreads();
+        w = 0;
+#pragma unroll
+        for (int i = 0; i < kPlanWaves; ++i) w += work[i];
+        const unsigned long long room = plan.places - plan.units;
+        length = (int)max((unsigned long long)plan.least, (w + room - 1) / room);
+    }
+    if (tid == 0) plan.starts[0] = (uint32_t)length;
+    uint32_t before = 0;
+    for (int n0 = 0; n0 < a.num_seqs; n0 += kPlanThreads) {
+        const int n = n0 + tid;
+        int chunks;
+        uint32_t take = 0;
+        if (n < a.num_seqs) take = places_of(request_of(a, n, g, cols, keys), length, chunks);
+        uint32_t incl = take;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const uint32_t y = __shfl_up(incl, m, 64);
+            if (lane >= m) incl += y;
+        }
+        if (lane == 63) part[wave] = incl;
+        __syncthreads();
+        incl += before;
+#pragma unroll
+        for (int w = 0; w < kPlanWaves; ++w) {
+            if (w < wave) incl += part[w];
+            before += part[w];
+        }
+        if (n < a.num_seqs) plan.starts[1 + n] = incl - take;
+        __syncthreads();
+    }
+    if (tid == 0) plan.starts[1 + a.num_seqs] = before;
+}
+
+// What place p stands for, from the places' begins: a search 64 ways a step by
+// each wave for itself.
+__device__ Unit planned_unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int cols, int keys) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t *starts = plan.starts + 1;
+    Unit u{-1, 0, 0, 1, (int)plan.starts[0]};
+    if ((uint32_t)p >= starts[a.num_seqs]) return u;
+    int lo = 0, num = a.num_seqs;
+    while (num > 1) {
+        const int step = (num + 63) / 64, i = lane * step;
+        const unsigned long long m = __ballot(i < num && starts[lo + min(i, num - 1)] <= (uint32_t)p);
+        const int k = (63 - __builtin_clzll(m | 1)) * step;
+        lo += k;
+        num = min(step, num - k);
+    }
+    places_of(request_of(a, lo, g, cols, keys), u.length, u.chunks);
+    u.n = lo;
+    u.column = (int)(p - starts[lo]) / u.chunks;
+    u.chunk = (int)(p - starts[lo]) % u.chunks;
+    return u;
+}
+
+// The same (n < 0: nothing) from the lengths.
 __device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int cols, int keys) {
     __shared__ unsigned long long work[kWaves];
     __shared__ uint32_t part[kWaves];
@@ -133,9 +213,7 @@ __device__ Unit unit_of(const AttendArgs &a, const Plan &plan, int p, int g, int
         uint32_t take = 0;
         int chunks = 1;
         if (n < a.num_seqs) {
-            const Request r = request_of(a, n, g, cols, keys);
-            chunks = max(1, (r.tiles + u.length - 1) / u.length);
-            take = (uint32_t)r.units * chunks;
+            take = places_of(request_of(a, n, g, cols, keys), u.length, chunks);
         }
         uint32_t incl = take;
 #pragma unroll
@@ -265,7 +343,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
     float (*joined)[4][256] = reinterpret_cast<float (*)[4][256]>(pool);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, grp = lane >> 4;
     const int head = blockIdx.x % a.heads, place = blockIdx.x / a.heads, g = a.q_heads / a.heads;
-    const Unit u = !SPLIT && plan.places == plan.units && a.num_seqs <= 64 ? longest_unit_of(a, place, g, COLS, KEYS) : unit_of(a, plan, place, g, COLS, KEYS);
+    const Unit u = plan.starts ? planned_unit_of(a, plan, place, g, COLS, KEYS)
+                   : !SPLIT && plan.places == plan.units && a.num_seqs <= 64 ? longest_unit_of(a, place, g, COLS, KEYS)
+                                                                             : unit_of(a, plan, place, g, COLS, KEYS);
     if (u.n < 0) return;
     const Request r = request_of(a, u.n, g, COLS, KEYS);
     // the last columns first: they see the most keys
@@ -639,6 +719,7 @@ template <typename T, int D> __global__ __launch_bounds__(256) void join_kernel(
 
 template <typename T, int D, int NT, int KEYS, bool SPLIT>
 hipError_t launch(const AttendArgs &a, const Layout &y, const Plan &plan, hipStream_t stream) {
+    if (plan.starts) plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, plan, y.cols, KEYS);
     attend_kernel<T, D, NT, KEYS, SPLIT><<<(unsigned)(plan.places * a.heads), kThreads, 0, stream>>>(a, plan);
     if (plan.places > plan.units) {
         const long columns = (long)a.total_tokens * a.q_heads;
@@ -657,8 +738,8 @@ template <typename T, int D> hipError_t launch(const AttendArgs &a, const Layout
 
 size_t attend_workspace_bytes(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16) {
     const Layout y = layout_of(num_seqs, total_tokens, q_heads, heads, io_bf16);
-    if (y.places == y.units) return 0;
-    return info_bytes((long)total_tokens * q_heads) + (size_t)y.places * heads * y.cols * (d + 2) * sizeof(float);
+    if (y.places == y.units) return starts_bytes(num_seqs);
+    return starts_bytes(num_seqs) + info_bytes((long)total_tokens * q_heads) + (size_t)y.places * heads * y.cols * (d + 2) * sizeof(float);
 }
 
 long attend_grid(int num_seqs, int total_tokens, int q_heads, int heads, int d, bool io_bf16) {
@@ -678,8 +759,11 @@ hipError_t launch_attend(const AttendArgs &a, void *workspace, hipStream_t strea
     // but 128 where the undivided columns are no 96 workgroups (one of 1889 tokens over
     // 2 heads, 30 workgroups: 21 us, with 512 keys 27).
     plan.least = y.split ? 8 : y.units * a.heads < 96 ? 4 : a.io_bf16 ? 16 : 8;
-    plan.info = static_cast<int *>(workspace);
-    plan.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + info_bytes((long)a.total_tokens * a.q_heads));
+    char *at = static_cast<char *>(workspace);
+    if (starts_bytes(a.num_seqs)) plan.starts = reinterpret_cast<uint32_t *>(at);
+    at += starts_bytes(a.num_seqs);
+    plan.info = reinterpret_cast<int *>(at);
+    plan.parts = reinterpret_cast<float *>(at + info_bytes((long)a.total_tokens * a.q_heads));
     plan.sums = plan.parts + (size_t)y.places * a.heads * y.cols * a.d;
     if (a.io_bf16) return a.d == 64 ? launch<bf16, 64>(a, y, plan, stream) : launch<bf16, 128>(a, y, plan, stream);
     return a.d == 64 ? launch<float, 64>(a, y, plan, stream) : launch<float, 128>(a, y, plan, stream);
