@@ -24,6 +24,12 @@
 // of places: the chunk length follows from the lengths on the device, such that
 // the places always suffice and hold about equal work.  Chunks of one column
 // are joined by a second launch.
+//
+// Bound by HBM for single tokens and drafts (one token of 64 requests of 100 to
+// 16,000 tokens, 4 heads x 128: 547 MB in 111.5 us; four drafts of 128 requests, 16
+// heads x 64: 105 us, 5.2 TB/s), by vector and matrix instructions that hardly
+// overlap for prompts (4 of 2000 to 4096 tokens, 32 over 8 heads x 128: 667 us, 838
+// TFLOP/s, 68% of what a large bf16 product reaches).
 #include <algorithm>
 
 #include "kda_device.h"
@@ -77,7 +83,9 @@ struct Plan {
 
 // Up to this many requests every workgroup finds its place from the lengths by
 // itself, a request a thread, which takes about a microsecond; for more a launch
-// of one workgroup before them writes down where each request's places begin.
+// of one workgroup before them writes down where each request's places begin (1024
+// requests of 50 to 600 tokens over 8 heads 203 us, with every workgroup by itself
+// 281; 64 requests 115 and 111.5).
 constexpr int kFindOwn = kThreads;
 size_t starts_bytes(int num_seqs) { return num_seqs <= kFindOwn ? 0 : ((size_t)num_seqs * 4 + 8 + 255) / 256 * 256; }
 size_t info_bytes(long columns) { return ((size_t)columns * 8 + 255) / 256 * 256; }

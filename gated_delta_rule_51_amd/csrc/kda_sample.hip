@@ -19,6 +19,11 @@
 // bin a cut lies, that bin's few logits are gathered and put in order, and the
 // part that holds the token, known by its share of the weights, is gone through
 // again.  A third writes the probabilities where they are asked for.
+//
+// The first launch is bound by the vector units, that is by the weights in 64 bits
+// (256 rows of 65,536 in bf16 21.5 us; with counts alone, 128 rows of 50,001 in fp32,
+// 12), the second by the latency of one workgroup a row (one row of 131,072 27 us,
+// 256 rows 33), the third by HBM (128 x 50,001 13.5 us, 3.8 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -240,7 +245,7 @@ __device__ __forceinline__ Limits limits_of(const SampleArgs &a, long n) {
 }
 
 // kCopies histograms side by side, a lane's by its number, keep lanes that meet in
-// a bin apart.
+// a bin apart (256 rows of 65,536: 22 us, with one 43).
 constexpr int kCopies = 4;
 template <typename T> __global__ __launch_bounds__(kPartThreads) void parts_kernel(const SampleArgs a, const Work w, int bits) {
     __shared__ uint32_t count[kBins * kCopies];

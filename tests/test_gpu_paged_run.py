@@ -339,3 +339,21 @@ def test_many_requests(K):
     o = K.kv_attention(q, up(cu), up(totals), up(at), up(table), *cache.all())
     ref, tol = R.attention(f64(q), cu, totals, at, table, values(cache.kc), values(cache.vc), f64(cache.ks), f64(cache.vs), D ** -0.5, BF)
     R.check("o", o, ref, tol, BF)
+
+
+def test_many_prompts(K):
+    """More requests than a workgroup's threads with prompts, some empty, one long."""
+    r = random.Random(8)
+    n, bs, H, Hq, D = 290, 32, 1, 2, 64
+    lens = [r.choice([0, 17, 40, 55]) for _ in range(n)]
+    old = [r.randint(0, 20) for _ in range(n)]
+    lens[100], old[100], old[200] = 600, 300, 900
+    g = torch.Generator().manual_seed(8)
+    blocks = sum(-(-(a + b) // bs) for a, b in zip(lens, old)) + 2
+    table, at, cu = layout(lens, old, bs, blocks, 8)
+    cache = filled(K, table, at, lens, old, blocks, H, bs, D, g)
+    q = torch.randn(int(cu[-1]), Hq, D, generator=g).to(BF).cuda()
+    totals = [a + b for a, b in zip(lens, old)]
+    o = K.kv_attention(q, up(cu), up(totals), up(at), up(table), *cache.all())
+    ref, tol = R.attention(f64(q), cu, totals, at, table, values(cache.kc), values(cache.vc), f64(cache.ks), f64(cache.vs), D ** -0.5, BF)
+    R.check("o", o, ref, tol, BF)
