@@ -79,6 +79,9 @@ def test_ties(K, io):
     for p in (1e-4, 0.3, 0.5, 0.99):
         both(K, x, u, p=[p] * n)
         both(K, x, u, k=[5000] * n, p=[p] * n)
+        both(K, x, u, p=[p] * n, m=[0.2] * n)
+    both(K, x, u, m=[0.5] * n)
+    both(K, x, u, k=[3000] * n, m=[0.9] * n)
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
@@ -98,6 +101,9 @@ def test_odd_logits(K, io):
     both(K, x, u)
     both(K, x, u, t=[0.0] * 9)
     both(K, x, u, k=[400] * 9, p=[0.8] * 9)
+    both(K, x, u, m=[0.05] * 9)
+    both(K, x, u, k=[30] * 9, m=[0.3] * 9)
+    both(K, x, u, p=[0.9] * 9, m=[1e-9] * 9)
     both(K, x, u, t=[1e-20, 1e-20, 1e30, 1.0, 1e-3, 1e25, 1e-38, 1e-20, 3e38], p=[0.9] * 9)
 
 
@@ -123,6 +129,8 @@ def test_large(K, io, v):
     x, u = logits(2, v, io, 5)
     both(K, x, u, t=[0.8, 1.2], p=[0.9, 0.99])
     both(K, x, u, k=[50, 5000], p=[0.9, 0.99])
+    both(K, x, u, k=[2000, 1025], m=[0.01, 1e-3])
+    both(K, x, u, k=[1024, 700], p=[0.999, 1.0], m=[1e-4, 0.0])
 
 
 def test_many_rows_alike(K):
