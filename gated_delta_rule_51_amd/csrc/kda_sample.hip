@@ -927,13 +927,16 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
         }
         int part = 0;
         for (; part < kWaves - 1 && sh.sums[part] <= want; ++part) want -= sh.sums[part];
+        if (sh.sums[part] <= want) {   // sums of parts and of their logits may differ in the last place: the last one that weighs
+            while (part > 0 && sh.sums[part] == 0) --part;
+            want = max(sh.sums[part], (u64)1) - 1;
+        }
         lo = min(lo + part * each, hi);
         hi = min(lo + each, hi);
         __syncthreads();
     }
     if (wave == 0) {
         const u64 own = lo + lane < hi ? kept(value(x, lo + lane), lo + lane) : 0, incl = wave_running(own);
-        // the sums of parts and of their logits may differ in the last place: then the last one that weighs
         const u64 past = __ballot(incl > want), some = __ballot(own > 0);
         if (lane == 0) a.tokens[n] = lo + (past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : 0);
     }
