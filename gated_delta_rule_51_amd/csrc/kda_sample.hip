@@ -875,7 +875,11 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
 #pragma unroll
         for (int k = 0; k < EACH; ++k) {
             const int p = own_part + k * QUARTER;
-            if (p >= w.parts || sh.factor[p] < 0.0) continue;
+            // A part whose largest logit is below half a unit of the row (or has none) holds
+            // nothing that could be drawn, though its own sum, in finer units, may round to
+            // one and more.  In any other part that has logits before the cut's bin its
+            // largest is one of them, so a part with a sum has a logit that weighs.
+            if (p >= w.parts || !(sh.factor[p] * row.one > 0.5)) continue;
             const u64 s = wave_sum(edge == kBins || min(own_bin + sh.shift[p], kBins - 1) < edge ? part_mass[k] : 0);
             if (lane == 0 && s) atomicAdd(&sh.part_mass[p], (u64)__builtin_rint((double)s * sh.factor[p]));
         }
@@ -937,8 +941,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
     }
     if (wave == 0) {
         const u64 own = lo + lane < hi ? kept(value(x, lo + lane), lo + lane) : 0, incl = wave_running(own);
-        const u64 past = __ballot(incl > want), some = __ballot(own > 0);
-        if (lane == 0) a.tokens[n] = lo + (past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : 0);
+        const u64 past = __ballot(incl > want), some = __ballot(own > 0);   // some: never none
+        if (lane == 0) a.tokens[n] = lo + (past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some | 1));
     }
 }
 

@@ -708,7 +708,8 @@ typedef struct {
  * zeros; where the largest is infinite, those that equal it share all weight.
  * Weights are formed in fp64 and summed as multiples of 2^-46 (2^-45 over 65,536
  * tokens, and so on), so that a token and its cut are the same from call to call
- * and those of exact sums but where a border lies within that rounding.  Outputs
+ * and those of exact sums but where a border lies within that rounding.  A weight
+ * below half of such a multiple is none: its token is not drawn.  Outputs
  * overlap no input and not one another.  The workspace may be reused by calls that
  * are ordered on one stream; it may be NULL where its size is 0.
  */
