@@ -960,7 +960,8 @@ def kv_reserve(cu_seqlens, total_tokens, state_indices, kv_lens, blocks_held, bl
 def kv_commit(cu_seqlens, state_indices, kv_lens, blocks_held, *, block_size, steps=None):
     """The requests' new tokens count: kv_lens[row] grows by all of them, or with
     steps [N] (verify_drafts' accepted) by steps[n] + 1; left as it is where that is
-    not among the request's tokens or beyond its blocks."""
+    not among the request's tokens, and where kv_reserve refused the request (its
+    blocks do not hold all of its tokens)."""
     block_size = _block_size(block_size)
     if _run("kv_commit", cu_seqlens, steps, state_indices, kv_lens, blocks_held, block_size):
         return

@@ -594,10 +594,11 @@ kda_status kda_kv_reserve(const kda_pages_desc *desc, const int32_t *cu_seqlens,
 
 /*
  * kv_lens[row] grows by the request's tokens, or with steps [N] (as for
- * kda_commit_states: the accepted step of a run of drafts) by steps[n] + 1; a step
- * that is negative or not below the request's length, or a length beyond the
- * request's blocks, leaves it as it is.  Blocks of tokens that did not stand stay
- * with the request.  total_tokens, max_blocks and num_free play no part.
+ * kda_commit_states: the accepted step of a run of drafts) by steps[n] + 1.  A step
+ * that is negative or not below the request's length leaves it as it is, and so does
+ * a request whose blocks do not hold all of its tokens: kda_kv_reserve refused it, so
+ * none of them was stored, whichever step is given.  Blocks of tokens that did not
+ * stand stay with the request.  total_tokens, max_blocks and num_free play no part.
  */
 kda_status kda_kv_commit(const kda_pages_desc *desc, const int32_t *cu_seqlens,
                          const int32_t *steps, const int32_t *state_indices, int32_t *kv_lens,
