@@ -269,14 +269,16 @@ __device__ Unit longest_unit_of(const AttendArgs &a, int p, int g, int cols, int
         const long tokens = max((long)x - before, 0l);
         return r.units - (int)min((long)r.units, tokens * g / cols);
     };
-    int hi = r.total + cols;   // none see more
+    int hi = r.total + cols, lo = before;   // none see more; all do
 #pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) hi = max(hi, __shfl_xor(hi, m, 64));
+    for (int m = 32; m >= 1; m >>= 1) {
+        hi = max(hi, __shfl_xor(hi, m, 64));
+        lo = min(lo, __shfl_xor(lo, m, 64));
+    }
     Unit u{-1, 0, 0, 1, INT32_MAX / 2};
     if (p >= (int)wave_sum((uint32_t)r.units)) return u;
-    int lo = INT32_MIN / 2;    // all do
-    while (hi - lo > 1) {      // the least x that at most p units pass
-        const int x = lo + (hi - lo) / 2;
+    while ((uint32_t)hi - (uint32_t)lo > 1) {   // the least x that at most p units pass; apart by up to 2^32
+        const int x = lo + (int)(((uint32_t)hi - (uint32_t)lo) / 2);
         if ((int)wave_sum((uint32_t)past(x)) <= p) hi = x;
         else lo = x;
     }
