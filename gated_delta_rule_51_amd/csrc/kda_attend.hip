@@ -16,9 +16,14 @@
 // same reason.  e4m3 widens to bf16 exactly, and the block's power-of-two scale
 // goes in with it.
 //
-// Arithmetic: bf16 queries are operands as they are and p is rounded to bf16;
-// fp32 queries and their p go in as the sum of three bf16 terms.  Scores, sums
-// and outputs accumulate in fp32.
+// Arithmetic: bf16 queries are operands as they are.  p goes in as the sum of two
+// bf16 terms (16 bits) for single tokens and drafts, where memory leaves time for
+// it (64 tokens 112.2 us with one term and 112.5 with two, drafts 106 and 108, in two
+// column tiles 93 and 96; the error falls from 2.1e-3 to 1.66e-3, of which the
+// output's own rounding is 1.65e-3), and rounded to bf16, for its sum too, in the
+// kernel for prompts, whose registers a second term overflows (638 us with one,
+// 1241 with two).  fp32 queries and their p go in as the sum of three bf16 terms.
+// Scores, sums and outputs accumulate in fp32.
 //
 // Work is cut into (request, columns, chunk of keys) units over a fixed number
 // of places: the chunk length follows from the lengths on the device, such that
@@ -345,6 +350,7 @@ template <> struct Bytes<8> { u32x2 w; };
 template <typename T, int D, int NT, int KEYS, bool SPLIT>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void attend_kernel(const AttendArgs a, const Plan plan) {
     constexpr int TERMS = sizeof(T) == 4 ? 3 : 1, KL = D / 64, MT = D / 16, WAVE = 16 * NT, COLS = SPLIT ? WAVE : kWaves * WAVE;
+    constexpr int PTERMS = TERMS == 1 && SPLIT ? 2 : TERMS;         // of a numerator
     constexpr int ST = KEYS / 16, PS = KEYS / 32, OWN = KEYS / 4;   // score tiles, product steps, keys of a lane group
     constexpr bool QLDS = !SPLIT;
     constexpr int QBYTES = QLDS ? kWaves * NT * KL * 2 * TERMS * 1024 : 16, JOIN = kWaves * 4 * 256 * 4;
@@ -533,7 +539,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
                     for (int i = 0; i < 4; ++i) o[t][nt][i] *= f;
             }
         }
-        bf16x8 p[NT][PS][TERMS];
+        bf16x8 p[NT][PS];   // the numerators, where one term is all of them; more are formed where they are used
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float shift = -m[nt] * to2;
@@ -543,16 +549,16 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
                 for (int i = 0; i < 4; i += 2) {
                     const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][nt][i], to2, shift));
                     const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][nt][i + 1], to2, shift));
-                    if constexpr (TERMS == 1) {   // the sum of what the product sees, two at a time
+                    if constexpr (PTERMS == 1) {   // the sum of what the product sees, two at a time
                         const bf16x2 z{(__bf16)x, (__bf16)y};
-                        p[nt][t >> 1][0][4 * (t & 1) + i] = z[0];
-                        p[nt][t >> 1][0][4 * (t & 1) + i + 1] = z[1];
+                        p[nt][t >> 1][4 * (t & 1) + i] = z[0];
+                        p[nt][t >> 1][4 * (t & 1) + i + 1] = z[1];
                         l[nt] = __builtin_amdgcn_fdot2_f32_bf16(z, bf16x2{(__bf16)1.f, (__bf16)1.f}, l[nt], false);
                     } else {
                         l[nt] += x;
                         l[nt] += y;
-                        terms_of<TERMS>(x, 4 * (t & 1) + i, p[nt][t >> 1]);
-                        terms_of<TERMS>(y, 4 * (t & 1) + i + 1, p[nt][t >> 1]);
+                        s[t][nt][i] = x;
+                        s[t][nt][i + 1] = y;
                     }
                 }
         }
@@ -596,16 +602,33 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 && !SPLIT ? 1 : 2) void at
                     for (int i = 0; i < OWN / 4; ++i) vr[t].w[i] &= ~((nan_bytes(vr[t].w[i]) >> 7) * 0xffu);
             }
         }
+        if constexpr (PTERMS == 1) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int h = 0; h < PS; ++h) {
+                    const bf16x8 v = widen(vr[t].w[2 * h], vr[t].w[2 * h + 1], vs);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) o[t][nt] = mma(v, p[nt][h], o[t][nt]);
+                }
+        } else {
 #pragma unroll
             for (int h = 0; h < PS; ++h) {
-                const bf16x8 v = widen(vr[t].w[2 * h], vr[t].w[2 * h + 1], vs);
+                bf16x8 z[NT][PTERMS];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = TERMS - 1; i >= 0; --i) o[t][nt] = mma(v, p[nt][h][i], o[t][nt]);
+                    for (int e = 0; e < 8; ++e) terms_of<PTERMS>(s[2 * h + e / 4][nt][e % 4], e, z[nt]);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const bf16x8 v = widen(vr[t].w[2 * h], vr[t].w[2 * h + 1], vs);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = PTERMS - 1; i >= 0; --i) o[t][nt] = mma(v, z[nt][i], o[t][nt]);
+                }
             }
+        }
         load_v(next, vpage);
     }
 #pragma unroll

@@ -663,12 +663,14 @@ kda_status kda_kv_store(const kda_kv_desc *desc, const void *k, const void *v, c
  *   o          [T, Hq, D] io dtype, contiguous; rows past cu_seqlens[N] are not
  *              written; must not overlap any input
  * Precision: keys and values are exact in bf16, the matrix cores' operands.  bf16
- * queries are operands as they are, and softmax's numerators are rounded to bf16
- * (2^-8 of each) for the second product and for their sum alike; with fp32 io
- * queries and numerators go in as the sum of three bf16 terms, which hold all
- * their bits.  Scores, sums and outputs accumulate in fp32.  What a token does not
- * see has no part in its output, NaN or not.  Not checked: scores lie within
- * +-10^30.  Calls of the same sizes and lengths add in the same order.
+ * queries are operands as they are.  Softmax's numerators go into the second product
+ * as the sum of two bf16 terms (2^-16 of each) in calls of single tokens and drafts,
+ * T * Hq / Hk <= 32 * N.  In others they are rounded to bf16 (2^-8 of each), for the
+ * product and for their sum alike.  With fp32 io queries and numerators go in as the
+ * sum of three bf16 terms, which hold all their bits, in every call.  Scores, sums
+ * and outputs accumulate in fp32.  What a token does not see has no part in its
+ * output, NaN or not.  Not checked: values, the products q . k and the scores lie
+ * within +-10^30.  Calls of the same sizes and lengths add in the same order.
  * The workspace overlaps nothing else; it may be reused by calls that are ordered
  * on one stream.  T * Hq < 2^31.
  */
