@@ -81,7 +81,8 @@ template <bool SLOTS> __global__ __launch_bounds__(kThreads) void reserve_kernel
     const int tid = threadIdx.x, b = 1 << a.block_shift;
     const uint32_t count = (uint32_t)min(max(a.free_count[0], 0), a.num_free);
     uint32_t asked = 0, taken = 0;
-    for (int n0 = 0; n0 < a.num_seqs; n0 += kThreads) {
+    for (long first_n = 0; first_n < a.num_seqs; first_n += kThreads) {
+        const int n0 = (int)first_n;
         const int n = n0 + tid, some = min(kThreads, a.num_seqs - n0);
         int r = -1, have = 0, len = 0, begin = 0;
         long want = 0, total = 0;
@@ -163,7 +164,8 @@ __global__ __launch_bounds__(kThreads) void release_kernel(const PagesArgs a) {
     const uint32_t count = (uint32_t)min(max(a.free_count[0], 0), a.num_free);
     uint32_t all = 0, before = 0, top = 0;
     for (int pass = 0; pass < 2; ++pass) {   // how many there are, then where each goes
-        for (int n0 = 0; n0 < a.num_seqs; n0 += kThreads) {
+        for (long first_n = 0; first_n < a.num_seqs; first_n += kThreads) {
+            const int n0 = (int)first_n;
             const int n = n0 + tid, some = min(kThreads, a.num_seqs - n0);
             int r = -1, keep = 0, stay = 0;
             uint32_t give = 0;
@@ -222,13 +224,16 @@ __global__ __launch_bounds__(256) void commit_kernel(const PagesArgs a) {
 // too.
 constexpr int kSlotsAtOnce = 8192;
 
+// Workgroups of 256 for n items, up to 2^31 - 1 of them.
+static unsigned groups_of(int n) { return (unsigned)(((long)n + 255) / 256); }
+
 hipError_t launch_reserve(const PagesArgs &a, hipStream_t stream) {
     if (a.total_tokens <= kSlotsAtOnce) {
         reserve_kernel<true><<<1, kThreads, 0, stream>>>(a);
         return hipGetLastError();
     }
     reserve_kernel<false><<<1, kThreads, 0, stream>>>(a);
-    slots_kernel<<<(a.total_tokens + 255) / 256, 256, 0, stream>>>(a);
+    slots_kernel<<<groups_of(a.total_tokens), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -238,7 +243,7 @@ hipError_t launch_release(const PagesArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_kv_commit(const PagesArgs &a, hipStream_t stream) {
-    commit_kernel<<<(a.num_seqs + 255) / 256, 256, 0, stream>>>(a);
+    commit_kernel<<<groups_of(a.num_seqs), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

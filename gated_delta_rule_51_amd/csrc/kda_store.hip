@@ -248,7 +248,8 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads, 8) void stor
     const int more = R > 64 ? 4 : bs > 64 ? 3 : 2;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const int t = t0 + 64 * q + lane, s = q < more && t < a.total_tokens ? a.slots[t] : -1;
+        const uint32_t t = (uint32_t)t0 + 64 * q + lane;   // may pass 2^31
+        const int s = q < more && t < (uint32_t)a.total_tokens ? a.slots[t] : -1;
         const int up = __shfl_up(s, 1, 64), before = lane ? up : edge;
         edge = __builtin_amdgcn_readlane(s, 63);
         follows[q] = __ballot(s >= 0 && (s & (bs - 1)) && before == s - 1);
