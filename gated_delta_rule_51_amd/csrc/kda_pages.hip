@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256) void commit_kernel(const PagesArgs a) {
     const int s = a.steps ? a.steps[n] : L - 1;
     if (s < 0 || s >= L) return;
     // a reservation gives blocks to a request's run as a whole or not at all, and only then were its tokens stored
-    const long len = a.kv_lens[r];
+    const long len = max(a.kv_lens[r], 0);   // as the reservation counts it
     if (len + L <= min((long)a.blocks_held[r] << a.block_shift, (long)INT32_MAX)) a.kv_lens[r] = (int)(len + s + 1);
 }
 

@@ -62,6 +62,17 @@ def test_row_too_short(K):
     assert b.lens.tolist() == [30, 0]
 
 
+@pytest.mark.parametrize("steps,want", [(None, 17), ([4], 5)])
+def test_length_nobody_filled(K, steps, want):
+    """A negative length counts as none for the reservation, and so for what follows."""
+    lens, held, table = up([-3]), up([0]), up([[-1, -1]])
+    free, count = up([4, 2]), up([2])
+    slots, totals = K.kv_reserve(up([0, 17]), 17, up([0]), lens, held, table, free, count, block_size=16)
+    assert totals.tolist() == [17] and slots.tolist() == [32 + i for i in range(16)] + [64]
+    K.kv_commit(up([0, 17]), up([0]), lens, held, block_size=16, steps=None if steps is None else up(steps))
+    assert lens.tolist() == [want]
+
+
 @pytest.mark.parametrize("bs", [16, 32, 64, 128])
 @pytest.mark.parametrize("seed", [3, 4, 5])
 def test_histories(K, bs, seed):
