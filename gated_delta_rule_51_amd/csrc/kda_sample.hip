@@ -519,7 +519,7 @@ __device__ u64 nth(Shared &sh, const Each &each, uint32_t lo, uint32_t hi, int V
         }
         __syncthreads();
         lo += (uint32_t)d << s;
-        hi = min(hi, lo + ((1u << s) - 1));
+        hi = lo + min(hi - lo, (1u << s) - 1);   // the piece's end itself may lie past 2^32
         if (s == 0) {                // one key, and more than a few that have it
             equal = lo;
             tie = true;
