@@ -141,6 +141,10 @@ __device__ __forceinline__ void fill_roots(double *root, int bits) {
     if (threadIdx.x < 64) root[threadIdx.x] = kRoots[threadIdx.x] * (double)(1ull << bits);
 }
 
+// NaN is no logit, and minus infinity weighs nothing wherever a limit cuts: neither is
+// counted or listed.  Whoever counts and whoever lists have to leave out the same.
+__device__ __forceinline__ bool counted(float x) { return x > -__builtin_inff(); }
+
 // What falls as x rises, 0 at the largest; both zeros are one.
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t b = x == 0.f ? 0 : __float_as_uint(x);
@@ -281,7 +285,7 @@ template <typename T> __global__ __launch_bounds__(kPartThreads) void parts_kern
     const int first = row.bin(top), copy = tid & (kCopies - 1);
     const auto count_all = [&](auto counts, auto weighs) {
         each_of<kPartThreads, 2>(x, lo, hi, [&](float y, int) {
-            if (y != y) return;
+            if (!counted(y)) return;
             const int b = (int)min((uint32_t)(first - row.bin(y)), (uint32_t)kBins - 1) * kCopies + copy;
             if constexpr (decltype(counts)::value) atomicAdd(&count[b], 1u);
             if constexpr (decltype(weighs)::value) atomicAdd(&mass[b], row.weight(y));
@@ -542,7 +546,7 @@ template <typename Holds> __device__ __forceinline__ uint32_t last_key(uint32_t 
     }
     return lo;
 }
-constexpr uint32_t kMinusInfinity = 0xff800000u;   // its key: the last of all
+constexpr uint32_t kLowest = 0xff7fffffu;   // the key of the lowest finite number: the last that counts
 
 // The row's logits in [from, to] into sh.list, with their weights; as many as the
 // caller has counted.
@@ -604,7 +608,7 @@ template <typename T> __device__ u64 cut_of_whole_row(Shared &sh, const Row &row
     __syncthreads();
     for (int i = tid; i < V; i += kThreads) {
         const float y = value(x, i);
-        if (y != y) continue;
+        if (!counted(y)) continue;
         const int b = bin(y);
         atomicAdd(&sh.count[b], 1u);
         atomicAdd(&sh.mass[b], row.weight(y));
@@ -614,10 +618,10 @@ template <typename T> __device__ u64 cut_of_whole_row(Shared &sh, const Row &row
         const auto each = [&](auto f) {
             for (int i = tid; i < V; i += kThreads) {
                 const float y = value(x, i);
-                if (y == y && bin(y) == b) f(place_of<T>(y, i), [&] { return row.weight(y); });
+                if (counted(y) && bin(y) == b) f(place_of<T>(y, i), [&] { return row.weight(y); });
             }
         };
-        return nth<T, decltype(by_mass)::value, false>(sh, each, cut_key<T>(key_of(row.top)), cut_key<T>(kMinusInfinity), V, want, upto);
+        return nth<T, decltype(by_mass)::value, false>(sh, each, cut_key<T>(key_of(row.top)), cut_key<T>(kLowest), V, want, upto);
     };
     u64 cut = ~0ull, before, upto = 0;
     int last = kFine;
@@ -723,7 +727,7 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
     if (lim.by_m) {                  // the smallest number whose weight is not below the limit
         if (wave == 0) {
             const double least = (double)lim.min_p * row.one;
-            const uint32_t k = last_key(key_of(top), kMinusInfinity, [&](uint32_t k) { return row.real(of_key(k)) >= least; });
+            const uint32_t k = last_key(key_of(top), kLowest + 1, [&](uint32_t k) { return row.real(of_key(k)) >= least; });
             if (lane == 0) sh.out[0] = last_of_key<T>(k);
         }
         __syncthreads();
@@ -732,8 +736,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
     }
     // the smallest logit of bins up to b (b >= 0)
     const auto end_of = [&](int b) {
-        if (b >= kBins - 1) return kMinusInfinity;
-        return last_key(key_of(top), kMinusInfinity + 1, [&](uint32_t k) { return bin(of_key(k)) <= b; });
+        if (b >= kBins - 1) return kLowest;
+        return last_key(key_of(top), kLowest + 1, [&](uint32_t k) { return bin(of_key(k)) <= b; });
     };
     const auto listed_each = [&](auto f) {
         const int some = sh.listed;
