@@ -214,3 +214,42 @@ def test_many_chunks(K, n, io):
     if n == 3:
         b = Batch(K, [45, 1], [40000, 3], 2, 2, 128, 64, io, n)
         b.check("prompt", b.run())
+
+
+def test_captured_and_on_streams(K):
+    """Undivided prompts, cut prompts and many requests in one graph, replayed with other
+    queries and eager work between, and on two streams at once: each equals its lone
+    call."""
+    works = [Batch(K, [1700, 0, 400], [0, 9, 50], 8, 64, 64, 64, BF, 1), Batch(K, [200, 90], [300, 2000], 2, 8, 128, 32, BF, 2),
+             Batch(K, [40] * 259, [3] * 259, 2, 6, 64, 16, F32, 3), Batch(K, [4] * 30, [700] * 30, 2, 8, 128, 16, BF, 4)]
+    assert undivided(K, *works[0].shape) and not undivided(K, *works[1].shape) and undivided(K, *works[2].shape)
+    fixed = [(up(b.cu), up(b.totals), up(b.at), up(b.table), *b.cache.all()) for b in works]
+    want = [[], []]
+    queries = [[b.q.clone(), b.q.roll(1, 0).contiguous()] for b in works]
+    for i in (0, 1):
+        want[i] = [K.kv_attention(q[i], *f) for q, f in zip(queries, fixed)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for b, f in zip(works, fixed):
+            K.kv_attention(b.q, *f)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [K.kv_attention(b.q, *f) for b, f in zip(works, fixed)]
+    for n in range(6):
+        for b, q in zip(works, queries):
+            b.q.copy_(q[n % 2])
+        graph.replay()
+        for o, w in zip(outs, want[n % 2]):
+            assert torch.equal(o, w), n
+        torch.empty(1 << 22, device="cuda").fill_(float("nan"))
+    streams, got = [torch.cuda.Stream() for _ in works], []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for q, f, w, s in zip(queries, fixed, want[0], streams):
+            with torch.cuda.stream(s):
+                got.append((K.kv_attention(q[0], *f), w))
+    torch.cuda.synchronize()
+    for o, w in got:
+        assert torch.equal(o, w)
