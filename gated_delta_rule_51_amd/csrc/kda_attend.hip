@@ -31,10 +31,10 @@
 // are joined by a second launch.
 //
 // Bound by HBM for single tokens and drafts (one token of 64 requests of 100 to
-// 16,000 tokens, 4 heads x 128: 547 MB in 111.5 us; four drafts of 128 requests, 16
-// heads x 64: 105 us, 5.2 TB/s), by vector and matrix instructions that hardly
-// overlap for prompts (4 of 2000 to 4096 tokens, 32 over 8 heads x 128: 667 us, 838
-// TFLOP/s, 68% of what a large bf16 product reaches).
+// 16,000 tokens, 4 heads x 128: 547 MB in 112.5 us; four drafts of 128 requests, 16
+// heads x 64: 108 us, 5.1 TB/s), by vector instructions, nearly five beside each
+// matrix one, for prompts (4 of 2000 to 4096 tokens, 32 over 8 heads x 128: 624 to 638
+// us, 896 TFLOP/s, 73% of what a large bf16 product reaches).
 #include <algorithm>
 
 #include "kda_device.h"
@@ -69,6 +69,13 @@ Layout layout_of(int num_seqs, int total_tokens, int q_heads, int heads, bool io
     y.keys = y.split ? 64 : 32;
     y.cols = 16 * y.nt * (y.split ? 1 : kWaves);
     y.units = columns / y.cols + num_seqs;
+    // Prompts are cut where their undivided units are fewer than two workgroups a CU.
+    // Cutting lets uneven contexts end together (6 prompts of 200 to 700 tokens behind up
+    // to 16,000, 328 workgroups: 410 us cut, 649 whole) and costs even ones the join (2 of
+    // 1000 to 1600, 376 workgroups: 156 and 114; 8 of up to 700, 464: 153 and 93); from 512 on whole was faster throughout
+    // (16 of 50 to 500 behind up to 2000, 656: 234 and 145; 3 of 500 to 2000 behind up to
+    // 8000, 552: 441 and 415).  Room for chunks: with half of 1024 the six prompts take
+    // 495 us, with twice that 454.
     long more = 0;
     if (y.split) more = std::max<long>((768 + heads - 1) / heads, y.units / 4);
     else if (y.units * heads < 512) more = (1024 + heads - 1) / heads;
@@ -89,8 +96,8 @@ struct Plan {
 // Up to this many requests every workgroup finds its place from the lengths by
 // itself, a request a thread, which takes about a microsecond; for more a launch
 // of one workgroup before them writes down where each request's places begin (1024
-// requests of 50 to 600 tokens over 8 heads 203 us, with every workgroup by itself
-// 281; 64 requests 115 and 111.5).
+// requests of 50 to 600 tokens over 8 heads 204 us, with every workgroup by itself
+// 281; 64 requests 115 with it, 112 without).
 constexpr int kFindOwn = kThreads;
 size_t starts_bytes(int num_seqs) { return num_seqs <= kFindOwn ? 0 : ((size_t)num_seqs * 4 + 8 + 255) / 256 * 256; }
 size_t info_bytes(long columns) { return ((size_t)columns * 8 + 255) / 256 * 256; }

@@ -11,6 +11,8 @@
 // up to 65,536 logits, one less for every doubling): such sums do not depend on
 // their order, so histograms may be filled by atomics and a token is the same
 // from call to call.  A weight below 2^-(B + 1) of the largest weighs nothing.
+// Neither does minus infinity, which masked rows are full of: it is left out from the
+// start (one row of 131,072 with 20 tokens allowed, top_k 50: 24 us, unmasked 28).
 //
 // Two launches.  The first cuts rows into parts, over the whole chip: each
 // part's largest logit, and a histogram of counts and weights over bins of
@@ -592,7 +594,9 @@ template <typename T> __device__ __forceinline__ void gather(Shared &sh, const R
 
 // The cut of a row whatever its logits, from passes over all of it: for rows
 // with more logits in the cut's bin than the list holds (thousands of equal
-// ones, or a cut far down).
+// ones, weights so flat that a cut lies far down).  One workgroup's latency: a row of
+// 131,072 normal logits at temperature 5 with top_p 0.9 takes 262 us, 256 such rows
+// 449; equal logits, which meet in one bin's atomics, 1.5 ms.
 template <typename T> __device__ u64 cut_of_whole_row(Shared &sh, const Row &row, const Limits &lim, const T *x, int V) {
     const int tid = threadIdx.x;
     // bins of (top - x) / T, 64 a unit

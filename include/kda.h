@@ -654,7 +654,9 @@ kda_status kda_kv_store(const kda_kv_desc *desc, const void *k, const void *v, c
  * n stands at position kv_totals[n] - L + j and sees the positions up to it:
  *     o = sum_i softmax_i(scale q . k_i) v_i
  * query head h over key head h / (Hq / Hk).  A token that sees nothing gives
- * zeros.  One token a request, runs of drafts and prompts, in any mixture.
+ * zeros.  One token a request, runs of drafts and prompts, in any mixture; the
+ * call's average length decides how all of them are cut, so prompts and single
+ * tokens behind long contexts may be faster in calls of their own.
  *   q          [T, Hq, D] io dtype, token rows q_stride elements apart (a multiple
  *              of 16 bytes)
  *   kv_totals  [N] int32; more than the row's blocks hold counts as that
@@ -672,7 +674,9 @@ kda_status kda_kv_store(const kda_kv_desc *desc, const void *k, const void *v, c
  * output, NaN or not.  Not checked: values, the products q . k and the scores lie
  * within +-10^30.  Calls of the same sizes and lengths add in the same order.
  * The workspace overlaps nothing else; it may be reused by calls that are ordered
- * on one stream.  T * Hq < 2^31.
+ * on one stream.  It holds partial sums of as many columns as the kernel could cut:
+ * for single tokens about 80 N Hk (D + 2) bytes and 6 MB (28 MB for 256 requests over 8
+ * heads of 128, 1.4 GB for 4096 over 32), none for large prompts.  T * Hq < 2^31.
  */
 size_t kda_kv_attention_workspace_size(const kda_kv_desc *desc);
 kda_status kda_kv_attention(const kda_kv_desc *desc, const void *q, const int32_t *cu_seqlens,
@@ -707,8 +711,9 @@ typedef struct {
  *               alone
  *   probs       [N, V] fp32, contiguous, or NULL: w over the sum of those kept, 0
  *               for the others: the distributions that kda_verify_drafts takes
- * A NaN logit is none.  A row without any logit above minus infinity gives -1 and
- * zeros; where the largest is infinite, those that equal it share all weight.
+ * A NaN logit is none; minus infinity weighs nothing and is never drawn, also where
+ * top_k takes more than there is besides.  A row without any logit above it gives -1
+ * and zeros; where the largest is infinite, those that equal it share all weight.
  * Weights are formed in fp64 and summed as multiples of 2^-46 (2^-45 over 65,536
  * tokens, and so on), so that a token and its cut are the same from call to call
  * and those of exact sums but where a border lies within that rounding.  A weight
