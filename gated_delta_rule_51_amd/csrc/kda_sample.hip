@@ -793,7 +793,8 @@ template <typename T> __global__ __launch_bounds__(kThreads) void choose_kernel(
                 u64 all, upto;
                 if (some > lim.top_k) {
                     cut = min(cut, nth<T, false, false>(sh, listed_each, key_lo, cut_key<T>(end), V, (u64)lim.top_k, all));
-                } else {
+                } else {   // all that are listed; others may follow
+                    cut = min(cut, last_of_key<T>(end));
                     u64 s = 0;
                     listed_each([&](u64, auto weight) { s += weight(); });
                     all = block_sum(sh, s);
